@@ -342,6 +342,144 @@ int64_t tara_packed_length(const tara_segment* segs, int32_t n_segs);
 int tara_pack_token_meta(const tara_segment* segs, int32_t n_segs,
                          uint8_t* seg, float* time_s, uint8_t* pic, float* m, int32_t N);
 
+/* ---- the layer around the attention ----------------------------------------------------- */
+/* Operators between a transformer's token stream x [B][N][C] and the Q, K, V of the attention,
+ * and between its O and the stream: rotary tables over several axes, per-head norms of Q and K
+ * with the rotation in the same pass, a linear layer with its epilogue, and the projection that
+ * does all of it at once.  The pages give neither the model's projections nor its rotary
+ * layout (they only say that the guide's rotary clock starts at the output's), so the axes,
+ * frequencies, pairing, norms and sizes are arguments.
+ *
+ * A strided view [B][H][N][D] of a device tensor: element (b, h, n, d) is at
+ * b*stride_b + h*stride_h + n*stride_n + d elements from ptr (strides of dimensions of size 1
+ * are ignored).  A token-major stream [B][N][C] is the view H = 1, D = C; a part of a fused
+ * projection [B][N][3][H][D] is a view with stride_h = D, stride_n = 3*H*D; the rows [a, e) of
+ * a packed [B][H][N][D] tensor are a view at ptr + a*D with N = e - a.  Column c of a row is
+ * (h, d) = (c / D, c % D).
+ *   - ptr 16-byte aligned; strides >= 0 and multiples of 16 bytes.  Only memory of the view's
+ *     own elements is read or written: rows behind N, and gaps between rows, stay as they are.
+ *   - a view that is written may not overlap itself, nor any view that is read except where an
+ *     entry point says so (TARA_ERR_PARAM for the same pointer; otherwise the caller's to see
+ *     to).                                                                                 */
+typedef struct {
+  void*      ptr;
+  tara_dtype dtype;
+  int32_t    B, H, N, D;
+  int64_t    stride_b, stride_h, stride_n;   /* elements */
+} tara_view;
+
+/* Rotary positions with several axes.  The first R = dim[0] + ... + dim[n_axes-1] columns of a
+ * head are rotated in R/2 pairs; axis a owns dim[a]/2 consecutive pairs, in axis order, and its
+ * i-th pair turns by position_a * theta[a]^(-2i/dim[a]).                                    */
+#define TARA_ROPE_MAX_AXES 4
+typedef struct {
+  int32_t n_axes;                       /* 1..4                                              */
+  int32_t dim[TARA_ROPE_MAX_AXES];      /* columns of each axis, even, >= 2; sum R <= 256    */
+  double  theta[TARA_ROPE_MAX_AXES];    /* > 0, finite                                       */
+} tara_rope;
+
+/* The (cos, sin) table of a packed sequence, computed once per shot and read by every layer.
+ *   pos   : device float array [n_rows][n_axes], finite; angles are formed in double
+ *           precision, so far positions keep their phase (|angle| up to 2^31 radians).
+ *   table : device float array [n_rows][R/2][2] (written), cos then sin; 16-byte aligned.
+ * Errors: TARA_ERR_NULL, TARA_ERR_SHAPE (n_rows < 1, a dim odd or < 2, R > 256 or not a
+ * multiple of 4), TARA_ERR_PARAM (n_axes or theta), TARA_ERR_ALIGN (pos 4 bytes),
+ * TARA_ERR_CUDA.  Asynchronous on `stream`.                                                */
+int tara_rope_table(const float* pos, int64_t n_rows, const tara_rope* rope, float* table,
+                    void* stream);
+
+typedef enum {
+  TARA_ROPE_INTERLEAVED = 0,   /* pair j is columns 2j and 2j + 1                            */
+  TARA_ROPE_HALVES      = 1    /* pair j is columns j and j + R/2                            */
+} tara_rope_pairing;
+
+/* What happens to each head's row of Q and K:
+ *   u = weight * x / sqrt(mean(x^2) + eps)                        if norm = 1 (else u = x)
+ *   (u_a, u_b) <- (u_a cos - u_b sin, u_a sin + u_b cos)          for every pair of the table
+ * with sums and products in fp32 and one rounding to the output's type.                    */
+typedef struct {
+  int32_t      norm;                /* 1: root-mean-square norm over D; 0: rotation only     */
+  float        eps;                 /* >= 0, finite                                          */
+  const void*  q_weight;            /* device, [D] or [H][D] of the tensors' dtype; NULL: 1  */
+  const void*  k_weight;
+  int64_t      weight_head_stride;  /* elements between heads' weights; 0: shared by heads   */
+  const float* table;               /* tara_rope_table's output, N rows; NULL: no rotation   */
+  int64_t      table_batch_stride;  /* floats between branches' tables; 0: one table         */
+  int32_t      rot_dim;             /* R: a multiple of 8 (interleaved) or 16 (halves), <= D  */
+  int32_t      pairing;             /* tara_rope_pairing                                     */
+} tara_norm_rope;
+
+/* Norm and rotation of Q and K in one pass over them.
+ *   q, k         : views of one shape and dtype (bf16, fp16, fp32), D a multiple of 8, <= 256.
+ *                  k (with k_out) may be NULL: only q is processed.
+ *   q_out, k_out : views of the same shape and dtype (written).  An output may be its own
+ *                  input (same ptr and strides).
+ * Weights and table 16-byte aligned, weight_head_stride and table_batch_stride multiples of
+ * 16 bytes.  Errors: TARA_ERR_NULL (also k without k_out), _SHAPE, _DTYPE, _HEAD_DIM (D),
+ * _PARAM (neither norm nor table, eps, rot_dim, pairing, overlapping views), _ALIGN,
+ * _TOO_LARGE (B or 2*H above 65535), TARA_ERR_CUDA.  Asynchronous on `stream`.             */
+int tara_qk_norm_rope(const tara_view* q, const tara_view* k, const tara_norm_rope* p,
+                      tara_view* q_out, tara_view* k_out, void* stream);
+
+typedef enum {
+  TARA_ACT_NONE      = 0,
+  TARA_ACT_GELU      = 1,   /* v/2 (1 + erf(v / sqrt 2))                                     */
+  TARA_ACT_GELU_TANH = 2,   /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))                 */
+  TARA_ACT_SILU      = 3    /* v / (1 + exp(-v))                                             */
+} tara_act;
+
+typedef struct {
+  const void*      bias;            /* device [C_out] of the tensors' dtype; NULL: none      */
+  int32_t          act;             /* tara_act                                              */
+  const void*      gate;            /* device [C_out], or per branch; NULL: 1                */
+  int64_t          gate_stride;     /* elements between branches' gates; 0: shared           */
+  const tara_view* residual;        /* NULL: none; same B, N and columns as y                */
+} tara_epilogue;
+
+/* y = residual + gate * act(x W^T + bias), accumulated in fp32, rounded once.
+ *   x : view with H*D = C_in columns (token-major, or the attention's O as it is).
+ *   w : device [C_out][C_in], rows contiguous, 16-byte aligned.
+ *   e : epilogue, NULL for none.  residual may be y itself (same ptr and strides).
+ *   y : view with H*D = C_out columns (written); token-major or head-major.
+ * One dtype throughout.  bf16/fp16: tensor cores; the D of every view a multiple of 8 (of 64
+ * where its H > 1).  fp32: an exact CUDA-core kernel, any sizes, pointers 4-byte aligned and
+ * strides free.  bias, gate 16-byte aligned, gate_stride a multiple of 16 bytes (16-bit types).
+ * Errors: TARA_ERR_NULL, _SHAPE, _DTYPE, _PARAM (act, a stride, overlapping views), _ALIGN,
+ * _TOO_LARGE, TARA_ERR_CUDA.  No workspace; asynchronous on `stream`.                      */
+int tara_linear(const tara_view* x, const void* w, const tara_epilogue* e, tara_view* y,
+                void* stream);
+
+/* The projection in front of the attention: [q | k | v] = x W^T + bias, q and k through the
+ * norm and rotation of tara_qk_norm_rope, all three written as views [B][H][N][D] (for instance
+ * rows of the packed tensors tara_attn_forward takes).
+ *   w : device [3*H*D][C_in]: the rows of q's heads, then k's, then v's.  bias [3*H*D] or NULL.
+ *   p : NULL: no norm and no rotation.
+ * bf16/fp16: D = 64 or 128.
+ * fp32: D as in tara_qk_norm_rope.  Other requirements and errors as for
+ * tara_linear and tara_qk_norm_rope.                                                       */
+int tara_qkv_project(const tara_view* x, const void* w, const void* bias,
+                     const tara_norm_rope* p, tara_view* q, tara_view* k, tara_view* v,
+                     void* stream);
+
+/* Positions of a packed sequence for tara_rope_table (host).  Grid g is `frames` x `rows` x
+ * `cols` tokens in row-major order (text: frames = length, rows = cols = 1); token (f, r, c)
+ * has on axis a the position origin[a] + f*frame_step[a] + r*row_step[a] + c*col_step[a],
+ * evaluated in double and rounded once to float.                                           */
+typedef struct {
+  int32_t frames, rows, cols;                       /* >= 1 */
+  double  origin[TARA_ROPE_MAX_AXES];
+  double  frame_step[TARA_ROPE_MAX_AXES];
+  double  row_step[TARA_ROPE_MAX_AXES];
+  double  col_step[TARA_ROPE_MAX_AXES];
+} tara_grid;
+
+/* Writes pos [N][n_axes] (host memory) for the grids in packing order.  Returns TARA_ERR_NULL,
+ * TARA_ERR_PARAM (n_axes not in 1..4), TARA_ERR_SEGMENT (a size < 1 or a non-finite number in
+ * the first n_axes entries), TARA_ERR_CAPACITY (N != total tokens) or TARA_OK.  Nothing is
+ * written unless the whole list is valid.                                                  */
+int tara_pack_token_positions(const tara_grid* grids, int32_t n_grids, int32_t n_axes,
+                              float* pos, int64_t N);
+
 #ifdef __cplusplus
 }
 #endif

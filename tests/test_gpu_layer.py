@@ -1,0 +1,330 @@
+"""The operators around the attention on the GPU against their fp64 definitions (oracle/layer.py).
+
+Tolerance of every element: the fp32 bound that comes with the definition, plus half a unit of
+the output's type (relative to value and bound), plus half the type's smallest subnormal.
+"""
+import numpy as np
+import pytest
+import torch
+
+import video_diffusion_attention_b200 as T
+from oracle import layer as ref
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+TINY = {"bf16": 0.0, "fp16": 2.0 ** -25, "fp32": 2.0 ** -149}
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def rand(shape, dtype, seed, scale=1.0, shift=0.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(shape, generator=g, dtype=torch.float32) * scale + shift
+    return x.to(DT[dtype]).cuda()
+
+
+def close(got, value, bound, dtype):
+    got = np64(got).reshape(value.shape)
+    half = torch.finfo(DT[dtype]).eps / 2
+    tol = bound + half * (np.abs(value) + bound) + TINY[dtype]
+    assert np.all(np.isfinite(got))
+    worst = np.max((np.abs(got - value) - tol))
+    assert worst <= 0, "beyond tolerance by %g (tolerance up to %g)" % (worst, tol.max())
+
+
+def positions(N, axes, seed, far=0.0):
+    g = np.random.Generator(np.random.PCG64(seed))
+    p = g.uniform(-20.0, 50.0, size=(N, axes)) + far
+    return torch.from_numpy(p.astype(np.float32)).cuda()
+
+
+def table_for(N, dims, seed, B=0):
+    """A random (cos, sin) table [N or B,N][R/2][2]."""
+    g = np.random.Generator(np.random.PCG64(seed))
+    a = g.uniform(-np.pi, np.pi, size=((B,) if B else ()) + (N, sum(dims) // 2))
+    return torch.from_numpy(np.stack([np.cos(a), np.sin(a)], -1).astype(np.float32)).cuda()
+
+
+# ---------------------------------------------------------------------------------------
+# rope_table
+# ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("N,dims,theta,far", [
+    (1, (64,), 10000.0, 0.0), (3, (2, 2), 10.0, 0.0), (257, (16, 56, 56), 10000.0, 0.0),
+    (1000, (44, 42, 42), 256.0, 1e6), (33, (64, 64, 64, 64), 1e6, -3e8),
+    (129, (128, 128), (500.0, 2e5), 2.0 ** 30), (5, (2, 120, 6), 1.0, 7e4),
+])
+def test_rope_table(N, dims, theta, far):
+    pos = positions(N, len(dims), N, far)
+    thetas = theta if isinstance(theta, tuple) else (theta,) * len(dims)
+    got = np64(T.rope_table(pos, dims, theta))
+    a = ref.angles(pos.cpu().numpy(), dims, thetas)
+    # the fp64 angle carries a few units of 2^-53 relative; what is left of it after the whole
+    # quarter turns is rounded to fp32 (at most pi/4 * 2^-24), then cos or sin to 2 units
+    tol = np.abs(a)[..., None] * 2.0 ** -50 + 2.0 ** -24 + 2 * 2.0 ** -23 * np.stack(
+        [np.abs(np.cos(a)), np.abs(np.sin(a))], -1)
+    want = np.stack([np.cos(a), np.sin(a)], -1)
+    assert got.shape == want.shape
+    assert np.all(np.abs(got - want) <= tol), np.max(np.abs(got - want))
+
+
+def test_rope_table_of_packed_positions_and_branches():
+    grids = [T.TokenGrid(frames=7), T.TokenGrid(3, 4, 5, origin=(7.0, 0.0, 0.0),
+                                                frame_step=(4 / 24, 0, 0))]
+    pos = torch.from_numpy(T.pack_token_positions(grids)).cuda()
+    one = T.rope_table(pos, (8, 12, 12))
+    both = T.rope_table(torch.stack([pos, pos + 1.0]), (8, 12, 12))
+    assert both.shape == (2, 67, 16, 2) and torch.equal(both[0], one)
+    assert torch.equal(one[0, :, 0], torch.ones(16, device="cuda"))       # position 0: no turn
+    out = torch.full((68, 16, 2), 7.0, device="cuda")
+    T.rope_table(pos, (8, 12, 12), out=out[:67])
+    assert torch.equal(out[:67], one) and bool((out[67] == 7.0).all())
+
+
+# ---------------------------------------------------------------------------------------
+# qk_norm_rope
+# ---------------------------------------------------------------------------------------
+def layout(kind, B, H, N, D, dtype, seed):
+    """Q or K of one layout, as a [B][H][N][D] view."""
+    if kind == "heads":
+        return rand((B, H, N, D), dtype, seed, 1.5)
+    if kind == "fused":
+        return rand((B, N, 3, H, D), dtype, seed, 1.5)[:, :, 1].transpose(1, 2)
+    if kind == "rows":                      # rows of a longer packed tensor
+        return rand((B, H, N + 13, D), dtype, seed, 1.5)[:, :, 5:5 + N]
+    return rand((B, 1, N, D), dtype, seed, 1.5).expand(B, H, N, D)      # one head, repeated
+
+
+QK_CASES = [
+    # B, H, N, D, dtype, layout, norm, weight, dims, halves
+    (1, 1, 1, 128, "bf16", "heads", True, "shared", (128,), False),
+    (1, 3, 1, 64, "fp16", "fused", True, "head", (16, 24, 24), True),
+    (2, 5, 33, 128, "bf16", "fused", True, "head", (16, 56, 56), False),
+    (2, 2, 67, 128, "bf16", "rows", True, "shared", (16, 56, 56), True),
+    (1, 2, 192, 64, "fp32", "heads", False, None, (24, 20, 20), False),
+    (3, 4, 17, 64, "fp32", "rows", True, "shared", (16, 16), True),      # half the head turns
+    (1, 7, 129, 128, "fp16", "heads", True, None, (8,), False),
+    (1, 2, 50, 256, "bf16", "fused", True, "shared", (256,), True),
+    (1, 2, 50, 96, "bf16", "heads", True, "head", (32, 32, 32), True),   # lanes left over
+    (2, 3, 40, 80, "fp32", "fused", True, "head", (16, 16), False),
+    (1, 2, 31, 8, "fp16", "heads", True, "shared", (8,), False),
+    (1, 3, 31, 24, "bf16", "heads", True, "shared", None, False),        # norm alone
+    (1, 4, 300, 128, "bf16", "repeat", True, "shared", (64,), True),
+    (1, 56, 130, 128, "bf16", "fused", True, "shared", (16, 56, 56), False),
+]
+
+
+@pytest.mark.parametrize("case", QK_CASES)
+def test_qk_norm_rope(case):
+    B, H, N, D, dtype, kind, norm, weight, dims, halves = case
+    q, k = layout(kind, B, H, N, D, dtype, 1), layout(kind, B, H, N, D, dtype, 2)
+    wq = wk = None
+    if weight:
+        shape = (H, D) if weight == "head" else (D,)
+        wq, wk = rand(shape, dtype, 3, 0.2, 1.0), rand(shape, dtype, 4, 0.2, 1.0)
+    table = table_for(N, dims, 5) if dims else None
+    qo, ko = T.qk_norm_rope(q, k, wq, wk, eps=1e-5, norm=norm, table=table,
+                            pairing="halves" if halves else "interleaved")
+    cs = np64(table) if dims else None
+    for x, w, y in ((q, wq, qo), (k, wk, ko)):
+        wn = 1.0 if w is None else (np64(w)[:, None, :] if w.dim() == 2 else np64(w))
+        value, bound = ref.norm_rope(np64(x), wn, float(np.float32(1e-5)), norm, cs, halves)
+        close(y, value, bound, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("halves", [False, True])
+def test_qk_norm_rope_in_place_and_gaps(dtype, halves):
+    # in place on a fused projection: V's columns and the rows outside the view stay
+    B, H, N, D = 2, 3, 37, 128
+    buf = rand((B, N + 4, 3, H, D), dtype, 9)
+    before = buf.clone()
+    q, k = (buf[:, 2:2 + N, i].transpose(1, 2) for i in range(2))
+    table = table_for(N, (16, 56, 56), 6, B)                      # a table per branch
+    pairing = "halves" if halves else "interleaved"
+    want = T.qk_norm_rope(q, k, table=table, pairing=pairing)
+    got = T.qk_norm_rope(q, k, table=table, pairing=pairing, q_out=q, k_out=k)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(buf[:, :, 2], before[:, :, 2])
+    assert torch.equal(buf[:, :2], before[:, :2]) and torch.equal(buf[:, 2 + N:], before[:, 2 + N:])
+    value, bound = ref.norm_rope(np64(before[:, 2:2 + N, 0].transpose(1, 2)), 1.0,
+                                 float(np.float32(1e-6)), True, np64(table)[:, None], halves)
+    close(got[0], value, bound, dtype)
+    # q alone gives the same
+    again = before[:, 2:2 + N, 0].transpose(1, 2)
+    assert torch.equal(T.qk_norm_rope(again, table=table, pairing=pairing), want[0])
+
+
+def test_qk_norm_rope_special_rows():
+    # a row of zeros stays zero, an infinity or a NaN stays in its own row
+    x = rand((1, 2, 20, 64), "bf16", 3)
+    x[0, 0, 3] = 0.0
+    x[0, 1, 7, 5] = float("inf")
+    x[0, 0, 9, 63] = float("nan")
+    table = table_for(20, (64,), 2)
+    y = T.qk_norm_rope(x, table=table)
+    assert bool((y[0, 0, 3] == 0).all())
+    bad = torch.isnan(y).any(-1)[0].cpu()
+    rows = {(0, 9), (1, 7)}
+    assert {(int(h), int(n)) for h, n in bad.nonzero()} == rows
+    # large and small values: the norm neither overflows nor vanishes in fp32
+    big = rand((1, 1, 4, 64), "bf16", 4) * 1e15
+    small = rand((1, 1, 4, 64), "bf16", 4) * 1e-15
+    for v in (big, small):
+        value, bound = ref.norm_rope(np64(v), 1.0, 0.0, True, None, False)
+        close(T.qk_norm_rope(v, eps=0.0), value, bound, "bf16")
+
+
+# ---------------------------------------------------------------------------------------
+# linear
+# ---------------------------------------------------------------------------------------
+def linear_inputs(B, N, K, C, dtype, xH, extras):
+    x = rand((B, xH, N, K // xH) if xH else (B, N, K), dtype, 11)
+    w = rand((C, K), dtype, 12, K ** -0.5)
+    o = {"bias": rand((C,), dtype, 13, 0.3) if "b" in extras else None,
+         "gate": rand((B, C), dtype, 14, 0.5, 0.5) if "g" in extras else
+         (rand((C,), dtype, 14, 0.5, 0.5) if "G" in extras else None),
+         "residual": rand((B, N, C), dtype, 15) if "r" in extras else None}
+    return x, w, o
+
+
+def linear_ref(x, w, o, act):
+    """[B][N][C] value and bound."""
+    x64 = np64(x)
+    if x64.ndim == 4:
+        x64 = x64.transpose(0, 2, 1, 3).reshape(x64.shape[0], x64.shape[2], -1)
+    vals = []
+    for b in range(x64.shape[0]):
+        g = o["gate"]
+        vals.append(ref.linear(
+            x64[b], np64(w), None if o["bias"] is None else np64(o["bias"]), act or "none",
+            None if g is None else (np64(g)[b] if g.dim() == 2 else np64(g)),
+            None if o["residual"] is None else np64(o["residual"][b])))
+    return np.stack([v for v, _ in vals]), np.stack([e for _, e in vals])
+
+
+LINEAR_CASES = [
+    # B, N, K, C, dtype, heads of x (0: token-major), extras, activation, heads of y
+    (1, 1, 128, 128, "bf16", 0, "", None, None),
+    (1, 1, 8, 8, "fp16", 0, "bgr", "silu", None),
+    (2, 1, 520, 1000, "bf16", 0, "bg", None, None),
+    (3, 5, 256, 136, "fp16", 0, "bgr", "gelu", None),
+    (1, 17, 72, 264, "bf16", 0, "b", "gelu_tanh", None),
+    (1, 64, 256, 256, "bf16", 2, "bGr", None, None),
+    (2, 65, 192, 384, "fp16", 3, "r", None, 6),
+    (1, 130, 1024, 128, "bf16", 8, "br", "silu", 1),
+    (1, 200, 448, 640, "bf16", 0, "b", None, 5),
+    (2, 257, 256, 512, "bf16", 2, "bgr", None, None),
+    (1, 300, 104, 776, "fp16", 0, "bg", "gelu", None),
+    (1, 513, 640, 264, "bf16", 0, "", "gelu_tanh", None),
+    (1, 1000, 512, 1536, "bf16", 4, "bgr", None, None),
+    (2, 700, 328, 520, "fp16", 0, "br", "silu", None),
+    (1, 2100, 256, 2304, "bf16", 0, "b", None, 18),
+    (1, 1, 1, 1, "fp32", 0, "bgr", "gelu", None),
+    (2, 33, 67, 101, "fp32", 0, "bgr", "silu", None),
+    (1, 192, 128, 512, "fp32", 2, "b", "gelu_tanh", None),
+    (3, 70, 129, 66, "fp32", 3, "r", None, 2),
+    (1, 5, 2000, 300, "fp32", 0, "bG", None, None),
+    (2, 500, 250, 404, "fp32", 0, "bgr", "gelu", None),
+]
+
+
+@pytest.mark.parametrize("case", LINEAR_CASES)
+def test_linear(case):
+    B, N, K, C, dtype, xH, extras, act, yH = case
+    x, w, o = linear_inputs(B, N, K, C, dtype, xH, extras)
+    y = T.linear(x, w, act=act, heads=yH, **o)
+    assert y.shape == ((B, yH, N, C // yH) if yH else (B, N, C))
+    value, bound = linear_ref(x, w, o, act)
+    if yH:
+        value, bound = (a.reshape(B, N, yH, -1).transpose(0, 2, 1, 3) for a in (value, bound))
+    close(y, value, bound, dtype)
+    assert T.device_status() == 0
+    # the same call gives the same bits
+    assert torch.equal(T.linear(x, w, act=act, heads=yH, **o), y)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("N", [1, 40, 300, 1030])
+def test_linear_views_and_gaps(dtype, N):
+    # x: columns of a wider stream; residual and y: rows of longer ones, y over the residual;
+    # everything outside y's rows and columns stays
+    B, K, C = 2, 256, 384
+    wide = rand((B, N, K + 64), dtype, 21)
+    x = wide[:, :, 32:32 + K]
+    w, bias = rand((C, K), dtype, 22, K ** -0.5), rand((C,), dtype, 23)
+    buf = rand((B, N + 9, C + 128), dtype, 24)
+    before = buf.clone()
+    y = buf[:, 4:4 + N, 64:64 + C]
+    o = {"bias": bias, "gate": None, "residual": before[:, 4:4 + N, 64:64 + C]}
+    value, bound = linear_ref(x, w, o, None)
+    got = T.linear(x, w, bias=bias, residual=y, out=y)
+    close(got, value, bound, dtype)
+    assert T.device_status() == 0
+    keep = torch.ones_like(buf, dtype=torch.bool)
+    keep[:, 4:4 + N, 64:64 + C] = False
+    assert torch.equal(buf[keep], before[keep])
+
+
+def test_linear_keeps_bad_rows_apart():
+    # infinities and NaN of one token stay in its row
+    for N in (6, 300):
+        x, w, _ = linear_inputs(1, N, 256, 512, "bf16", 0, "")
+        x[0, 3, 10] = float("nan")
+        x[0, 4, 11] = float("inf")
+        y = T.linear(x, w)
+        ok = torch.isfinite(y).all(-1)[0]
+        assert not ok[3] and not ok[4] and int(ok.sum()) == N - 2
+
+
+# ---------------------------------------------------------------------------------------
+# qkv_project
+# ---------------------------------------------------------------------------------------
+QKV_CASES = [
+    # B, N, K, H, D, dtype, heads of x, bias, norm, weight, dims, halves
+    (1, 40, 72, 2, 24, "fp32", 0, True, True, "shared", (8, 16), False),
+    (2, 9, 128, 3, 64, "fp32", 2, False, True, "head", (16, 24, 24), True),
+]
+
+
+def qkv_check(case):
+    B, N, K, H, D, dtype, xH, with_bias, norm, weight, dims, halves = case
+    x = rand((B, xH, N, K // xH) if xH else (B, N, K), dtype, 31)
+    w = rand((3 * H * D, K), dtype, 32, K ** -0.5)
+    bias = rand((3 * H * D,), dtype, 33, 0.3) if with_bias else None
+    wq = wk = None
+    if weight:
+        shape = (H, D) if weight == "head" else (D,)
+        wq, wk = rand(shape, dtype, 34, 0.2, 1.0), rand(shape, dtype, 35, 0.2, 1.0)
+    table = table_for(N, dims, 36) if dims else None
+    # outputs: rows of longer packed tensors, as another stream's tokens sit beside these
+    packed = [rand((B, H, N + 6, D), dtype, 37 + i) for i in range(3)]
+    before = [t.clone() for t in packed]
+    out = T.qkv_project(x, w, H, bias, wq, wk, eps=1e-6, norm=norm, table=table,
+                        pairing="halves" if halves else "interleaved",
+                        out=[t[:, :, 2:2 + N] for t in packed])
+    assert T.device_status() == 0
+    for t, b in zip(packed, before):
+        assert torch.equal(t[:, :, :2], b[:, :, :2]) and torch.equal(t[:, :, 2 + N:], b[:, :, 2 + N:])
+    x64 = np64(x)
+    if xH:
+        x64 = x64.transpose(0, 2, 1, 3).reshape(B, N, K)
+    cs = np64(table) if dims else None
+    for b in range(B):
+        v, e = ref.product(x64[b], np64(w), None if bias is None else np64(bias))
+        v, e = (a.reshape(N, 3, H, D).transpose(1, 2, 0, 3) for a in (v, e))
+        for i, wt in enumerate((wq, wk, None)):
+            if i == 2:
+                value, bound = v[i], e[i]
+            else:
+                wn = 1.0 if wt is None else (np64(wt)[:, None, :] if wt.dim() == 2 else np64(wt))
+                value, bound = ref.norm_rope(v[i], wn, float(np.float32(1e-6)), norm, cs, halves,
+                                             e[i])
+            close(out[i][b], value, bound, dtype)
+
+
+@pytest.mark.parametrize("case", QKV_CASES)
+def test_qkv_project(case):
+    qkv_check(case)

@@ -8,6 +8,10 @@ Alignment for MiniMax H3 References", "The temporal rule"), and output-video que
 to Picture i gain m*ln(gain_i) ("BFS H3 Reference Attention Binding (Experimental)",
 "The exact rule").  Returns O and the per-row log-sum-exp.
 
+Around it, the operators between a transformer's token stream and Q, K, V and between O and the
+stream: rotary tables over several axes, per-head norms of Q and K with the rotation, a linear
+layer with its epilogue, and the Q/K/V projection that joins them in one kernel.
+
 All compute runs in libtara_attn.so (C ABI in include/tara_attn.h); this package only
 marshals arguments.  Build the library with `python -m video_diffusion_attention_b200.build`.
 """
@@ -16,4 +20,7 @@ from ._binding import (  # noqa: F401
     make_params, pack_token_meta, packed_length, params_from, prepare_target_mask,
     quantize_qk_int8, selftest_wait, set_kernel_events, SEG_AUDIO, SEG_GUIDE,
     SEG_OTHER_VIDEO, SEG_PICTURE, SEG_TARGET, SEG_TEXT, TARA_BF16, TARA_FP16, TARA_FP32,
+)
+from ._layer import (  # noqa: F401
+    linear, pack_token_positions, qk_norm_rope, qkv_project, rope_table, TokenGrid,
 )

@@ -31,7 +31,8 @@ EXPORTS = ("tara_default_params", "tara_status_string", "tara_attn_forward",
            "tara_device_status", "tara_packed_length", "tara_pack_token_meta",
            "tara_set_kernel_events", "tara_selftest_wait", "tara_attn_forward_noalloc",
            "tara_prepare_target_mask", "tara_quantize_qk_int8", "tara_attn_forward_host",
-           "tara_debug_build")
+           "tara_debug_build", "tara_rope_table", "tara_qk_norm_rope", "tara_linear",
+           "tara_qkv_project", "tara_pack_token_positions")
 
 
 class TaraError(RuntimeError):
@@ -69,6 +70,41 @@ class TaraSegment(ctypes.Structure):
                 ("tokens_per_frame", ctypes.c_int32), ("pic", ctypes.c_int32),
                 ("t0_s", ctypes.c_double), ("frame_dt_s", ctypes.c_double),
                 ("mask", ctypes.c_void_p), ("mask_len", ctypes.c_int64)]
+
+
+class TaraView(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("dtype", ctypes.c_int), ("B", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("N", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_n", ctypes.c_int64)]
+
+
+ROPE_MAX_AXES = 4   # TARA_ROPE_MAX_AXES
+
+
+class TaraRope(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int32), ("dim", ctypes.c_int32 * ROPE_MAX_AXES),
+                ("theta", ctypes.c_double * ROPE_MAX_AXES)]
+
+
+class TaraNormRope(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("weight_head_stride", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("table_batch_stride", ctypes.c_int64),
+                ("rot_dim", ctypes.c_int32), ("pairing", ctypes.c_int32)]
+
+
+class TaraEpilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("act", ctypes.c_int32), ("gate", ctypes.c_void_p),
+                ("gate_stride", ctypes.c_int64), ("residual", ctypes.POINTER(TaraView))]
+
+
+class TaraGrid(ctypes.Structure):
+    _fields_ = [("frames", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("origin", ctypes.c_double * ROPE_MAX_AXES),
+                ("frame_step", ctypes.c_double * ROPE_MAX_AXES),
+                ("row_step", ctypes.c_double * ROPE_MAX_AXES),
+                ("col_step", ctypes.c_double * ROPE_MAX_AXES)]
 
 
 _lib = None
@@ -114,6 +150,23 @@ def load_library(path: Optional[str] = None):
     lib.tara_pack_token_meta.restype = ctypes.c_int
     lib.tara_pack_token_meta.argtypes = [ctypes.POINTER(TaraSegment), ctypes.c_int32] + [
         ctypes.c_void_p] * 4 + [ctypes.c_int32]
+    view = ctypes.POINTER(TaraView)
+    lib.tara_rope_table.restype = ctypes.c_int
+    lib.tara_rope_table.argtypes = [ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(TaraRope),
+                                    ctypes.c_void_p, ctypes.c_void_p]
+    lib.tara_qk_norm_rope.restype = ctypes.c_int
+    lib.tara_qk_norm_rope.argtypes = [view, view, ctypes.POINTER(TaraNormRope), view, view,
+                                      ctypes.c_void_p]
+    lib.tara_linear.restype = ctypes.c_int
+    lib.tara_linear.argtypes = [view, ctypes.c_void_p, ctypes.POINTER(TaraEpilogue), view,
+                                ctypes.c_void_p]
+    lib.tara_qkv_project.restype = ctypes.c_int
+    lib.tara_qkv_project.argtypes = [view, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.POINTER(TaraNormRope), view, view, view,
+                                     ctypes.c_void_p]
+    lib.tara_pack_token_positions.restype = ctypes.c_int
+    lib.tara_pack_token_positions.argtypes = [ctypes.POINTER(TaraGrid), ctypes.c_int32,
+                                              ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64]
     if path is None:
         _lib = lib
     return lib

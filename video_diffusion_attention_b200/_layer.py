@@ -1,0 +1,285 @@
+"""The operators around the attention (argument marshalling only, see include/tara_attn.h):
+rotary tables over several axes, the norm and rotation of Q and K, the linear layer and the
+Q/K/V projection.
+
+Tensors are CUDA tensors of one dtype (bf16, fp16 or fp32) on one device with the last dimension
+contiguous; other strides are passed on, so a part of a fused projection, a transposed view or
+rows of a packed tensor needs no copy.  Outputs the caller does not give are allocated on the
+stream the call runs on.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import dataclasses
+from typing import Optional, Sequence
+
+import numpy as np
+
+from ._binding import (ROPE_MAX_AXES, TaraEpilogue, TaraError, TaraGrid, TaraNormRope, TaraRope,
+                       TaraView, _dtype_code, load_library)
+
+ACTS = {None: 0, "none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3}
+PAIRINGS = {"interleaved": 0, "halves": 1}
+
+
+@dataclasses.dataclass
+class TokenGrid:
+    """`frames` x `rows` x `cols` tokens in packing order; token (f, r, c) has on axis a the
+    position origin[a] + f*frame_step[a] + r*row_step[a] + c*col_step[a].
+
+    The defaults give a video on (time, height, width); text of n tokens on the time axis is
+    TokenGrid(frames=n)."""
+    frames: int
+    rows: int = 1
+    cols: int = 1
+    origin: Sequence[float] = (0.0, 0.0, 0.0)
+    frame_step: Sequence[float] = (1.0, 0.0, 0.0)
+    row_step: Sequence[float] = (0.0, 1.0, 0.0)
+    col_step: Sequence[float] = (0.0, 0.0, 1.0)
+
+
+def pack_token_positions(grids: Sequence[TokenGrid], n_axes: int = 3) -> np.ndarray:
+    """Positions [N][n_axes] (float32, host) of the grids in packing order."""
+    arr = (TaraGrid * max(1, len(grids)))()
+    for c, g in zip(arr, grids):
+        c.frames, c.rows, c.cols = int(g.frames), int(g.rows), int(g.cols)
+        for name in ("origin", "frame_step", "row_step", "col_step"):
+            src, dst = getattr(g, name), getattr(c, name)
+            for a in range(min(n_axes, ROPE_MAX_AXES, len(src))):
+                dst[a] = float(src[a])
+    N = sum(max(0, int(g.frames)) * max(0, int(g.rows)) * max(0, int(g.cols)) for g in grids)
+    pos = np.empty((N, max(0, n_axes)), np.float32)
+    rc = load_library().tara_pack_token_positions(arr, len(grids), n_axes, pos.ctypes.data, N)
+    if rc != 0:
+        raise TaraError(rc, "tara_pack_token_positions")
+    return pos
+
+
+# ---------------------------------------------------------------------------------------
+# marshalling
+# ---------------------------------------------------------------------------------------
+def _view(t) -> TaraView:
+    """View of [B][H][N][D], [B][N][C] or [N][C] (any strides, last dimension contiguous)."""
+    nd = t.dim()
+    shape, stride = t.shape, t.stride()
+    if nd < 2 or nd > 4:
+        raise ValueError("expected [B][H][N][D], [B][N][C] or [N][C]")
+    if stride[-1] != 1 and shape[-1] != 1:
+        raise ValueError("the last dimension must be contiguous")
+    v = TaraView()
+    v.ptr, v.dtype = t.data_ptr(), _dtype_code(t)
+    v.N, v.D, v.stride_n = shape[-2], shape[-1], stride[-2]
+    v.B, v.stride_b = (shape[0], stride[0]) if nd > 2 else (1, 0)
+    v.H, v.stride_h = (shape[1], stride[1]) if nd > 3 else (1, 0)
+    return v
+
+
+def _vector(t, name: str, like, *shapes) -> Optional[int]:
+    """Pointer of an optional contiguous parameter of one of the given shapes."""
+    if t is None:
+        return None
+    if tuple(t.shape) not in shapes or not t.is_contiguous():
+        raise ValueError("%s must be contiguous of shape %s" % (name, " or ".join(map(str, shapes))))
+    if t.dtype != like.dtype:
+        raise TypeError("%s must have the tensors' dtype" % name)
+    _same_device(like, t)
+    return t.data_ptr()
+
+
+def _same_device(like, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != like.device:
+            raise ValueError("all tensors must be on one device")
+
+
+@contextlib.contextmanager
+def _launching(device, stream):
+    """The stream handle of a call, with `device` (and a stream that was given) current."""
+    import torch
+    with torch.cuda.device(device):
+        if stream is None:
+            yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        else:
+            with torch.cuda.stream(stream):
+                yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _check(rc: int, what: str) -> None:
+    if rc != 0:
+        raise TaraError(rc, what)
+
+
+def _cuda_only(*tensors) -> None:
+    for t in tensors:
+        if not t.is_cuda:
+            raise ValueError("expected CUDA tensors")
+
+
+# ---------------------------------------------------------------------------------------
+# the operators
+# ---------------------------------------------------------------------------------------
+def rope_table(pos, dims: Sequence[int], theta=10000.0, out=None, stream=None):
+    """(cos, sin) of every rotated pair: [..., N, sum(dims)/2, 2] float32 from positions
+    [..., N, axes] (float32, contiguous).  dims: columns of each axis; theta: one base or one
+    per axis."""
+    import torch
+    _cuda_only(pos)
+    if pos.dtype != torch.float32 or not pos.is_contiguous() or pos.dim() < 2:
+        raise ValueError("pos must be a contiguous float32 [..., N, axes] tensor")
+    n_axes = len(dims)
+    thetas = list(theta) if isinstance(theta, (list, tuple)) else [theta] * n_axes
+    if pos.shape[-1] != n_axes or len(thetas) != n_axes or n_axes > ROPE_MAX_AXES:
+        raise ValueError("pos, dims and theta must agree on the axes (at most %d)" % ROPE_MAX_AXES)
+    r = TaraRope()
+    r.n_axes = n_axes
+    for a in range(n_axes):
+        r.dim[a], r.theta[a] = int(dims[a]), float(thetas[a])
+    shape = tuple(pos.shape[:-1]) + (sum(int(d) for d in dims) // 2, 2)
+    with _launching(pos.device, stream) as s:
+        if out is None:
+            out = torch.empty(shape, dtype=torch.float32, device=pos.device)
+        elif tuple(out.shape) != shape or out.dtype != torch.float32 or not out.is_contiguous():
+            raise ValueError("out must be contiguous float32 of shape %s" % (shape,))
+        _same_device(pos, out)
+        _check(load_library().tara_rope_table(pos.data_ptr(), pos.numel() // max(1, n_axes),
+                                              ctypes.byref(r), out.data_ptr(), s),
+               "tara_rope_table")
+    return out
+
+
+def _norm_rope_struct(like, H, N, D, B, q_weight, k_weight, eps, norm, table, pairing):
+    p = TaraNormRope()
+    if pairing not in PAIRINGS:
+        raise ValueError("pairing must be one of %s" % sorted(PAIRINGS))
+    p.norm, p.eps, p.pairing = int(bool(norm)), eps, PAIRINGS[pairing]
+    if norm:
+        per_head = [w.dim() == 2 for w in (q_weight, k_weight) if w is not None]
+        if per_head and any(per_head) != all(per_head):
+            raise ValueError("q_weight and k_weight must both be [D] or both [H][D]")
+        p.q_weight = _vector(q_weight, "q_weight", like, (D,), (H, D))
+        p.k_weight = _vector(k_weight, "k_weight", like, (D,), (H, D))
+        p.weight_head_stride = D if per_head and per_head[0] else 0
+    elif q_weight is not None or k_weight is not None:
+        raise ValueError("weights are only used with the norm")
+    if table is not None:
+        import torch
+        if table.dtype != torch.float32 or not table.is_contiguous() or table.dim() not in (3, 4):
+            raise ValueError("table must be a contiguous float32 [N][R/2][2] or [B][N][R/2][2]")
+        if table.shape[-3] != N or table.shape[-1] != 2 or (table.dim() == 4 and table.shape[0] != B):
+            raise ValueError("table does not match the tokens")
+        _same_device(like, table)
+        p.table, p.rot_dim = table.data_ptr(), 2 * int(table.shape[-2])
+        p.table_batch_stride = table.stride(0) if table.dim() == 4 and B > 1 else 0
+    return p
+
+
+def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, eps: float = 1e-6, norm: bool = True,
+                 table=None, pairing: str = "interleaved", q_out=None, k_out=None, stream=None):
+    """q, k after the per-head root-mean-square norm (weights [D] or [H][D], None: 1) and the
+    rotation by `table` (None: none), in one pass over both.
+
+    q, k: [B][H][N][D] views with any strides; the outputs are new contiguous tensors unless
+    q_out / k_out are given (an output may be its own input).  k = None processes q alone and
+    returns one tensor."""
+    import torch
+    _cuda_only(q)
+    _same_device(q, k, q_out, k_out)
+    if q.dim() != 4:
+        raise ValueError("q must be [B][H][N][D]")
+    B, H, N, D = (int(x) for x in q.shape)
+    p = _norm_rope_struct(q, H, N, D, B, q_weight, k_weight, eps, norm, table, pairing)
+    with _launching(q.device, stream) as s:
+        if q_out is None:
+            q_out = torch.empty((B, H, N, D), dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty((B, H, N, D), dtype=q.dtype, device=q.device)
+        if k is None and k_out is not None:
+            raise ValueError("k_out without k")
+        ref = lambda t: ctypes.byref(_view(t)) if t is not None else None
+        _check(load_library().tara_qk_norm_rope(ref(q), ref(k), ctypes.byref(p), ref(q_out),
+                                                ref(k_out), s), "tara_qk_norm_rope")
+    return q_out if k is None else (q_out, k_out)
+
+
+def linear(x, w, bias=None, act: Optional[str] = None, gate=None, residual=None,
+           heads: Optional[int] = None, out=None, stream=None):
+    """residual + gate * act(x w^T + bias).
+
+    x: [N][C_in], [B][N][C_in], or [B][H][N][D] with C_in = H*D (the attention's output as it
+    is); w: [C_out][C_in]; bias [C_out]; gate [C_out] or [B][C_out]; act: None, "gelu",
+    "gelu_tanh" or "silu"; residual: columns of out in any of the layouts.  The result is
+    [N][C_out] or [B][N][C_out], or [B][heads][N][C_out/heads] when heads is given."""
+    import torch
+    _cuda_only(x)
+    _same_device(x, w, bias, gate, residual, out)
+    if act not in ACTS:
+        raise ValueError("act must be one of %s" % sorted(a for a in ACTS if a))
+    xv = _view(x)
+    if w.dim() != 2 or w.shape[1] != xv.H * xv.D or w.dtype != x.dtype or not w.is_contiguous():
+        raise ValueError("w must be contiguous [C_out][C_in] of x's dtype")
+    B, N, C = xv.B, xv.N, int(w.shape[0])
+    e = TaraEpilogue()
+    e.bias = _vector(bias, "bias", x, (C,))
+    e.act = ACTS[act]
+    e.gate = _vector(gate, "gate", x, (C,), (B, C))
+    e.gate_stride = C if gate is not None and gate.dim() == 2 and B > 1 else 0
+    rv = None
+    if residual is not None:
+        rv = _view(residual)
+        e.residual = ctypes.pointer(rv)
+    if heads is not None and (heads < 1 or C % heads != 0):
+        raise ValueError("heads must divide the output columns")
+    with _launching(x.device, stream) as s:
+        if out is None:
+            if heads is not None:
+                shape = (B, heads, N, C // heads)
+            else:
+                shape = (N, C) if x.dim() == 2 else (B, N, C)
+            out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        elif heads is not None and (out.dim() != 4 or out.shape[1] != heads):
+            raise ValueError("out must be [B][heads][N][D]")
+        yv = _view(out)
+        if yv.H * yv.D != C:
+            raise ValueError("out must have %d columns" % C)
+        _check(load_library().tara_linear(ctypes.byref(xv), w.data_ptr(), ctypes.byref(e),
+                                          ctypes.byref(yv), s), "tara_linear")
+    return out
+
+
+def qkv_project(x, w, heads: int, bias=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                norm: bool = True, table=None, pairing: str = "interleaved", out=None,
+                stream=None):
+    """q, k, v [B][heads][N][D] = x w^T + bias split into three, q and k through the norm and
+    rotation of qk_norm_rope (norm=False and table=None: neither).
+
+    x: [N][C_in], [B][N][C_in] or [B][H][N][D]; w: [3*heads*D][C_in]; out: three tensors or
+    views [B][heads][N][D] to write, for instance rows of the packed sequence's q, k, v."""
+    import torch
+    _cuda_only(x)
+    _same_device(x, w, bias)
+    xv = _view(x)
+    if w.dim() != 2 or w.shape[1] != xv.H * xv.D or w.dtype != x.dtype or not w.is_contiguous():
+        raise ValueError("w must be contiguous [3*heads*D][C_in] of x's dtype")
+    rows = int(w.shape[0])
+    if heads < 1 or rows % (3 * heads) != 0:
+        raise ValueError("w must have 3*heads*D rows")
+    B, N, D = xv.B, xv.N, rows // (3 * heads)
+    p = None
+    if norm or table is not None:
+        p = ctypes.byref(_norm_rope_struct(x, heads, N, D, B, q_weight, k_weight, eps, norm,
+                                           table, pairing))
+    elif q_weight is not None or k_weight is not None:
+        raise ValueError("weights are only used with the norm")
+    bias_ptr = _vector(bias, "bias", x, (rows,))
+    with _launching(x.device, stream) as s:
+        if out is None:
+            out = tuple(torch.empty((B, heads, N, D), dtype=x.dtype, device=x.device)
+                        for _ in range(3))
+        q, k, v = out
+        _same_device(x, q, k, v)
+        views = [_view(t) for t in (q, k, v)]
+        _check(load_library().tara_qkv_project(
+            ctypes.byref(xv), w.data_ptr(), bias_ptr, p, *(ctypes.byref(t) for t in views), s),
+            "tara_qkv_project")
+    return q, k, v

@@ -15,8 +15,8 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libtara_attn.so")
 # the same sources with the kernels' device-side checks compiled in (-DTARA_DEBUG=1)
 LIB_DEBUG = os.path.join(LIB_DIR, "libtara_attn_debug.so")
-SOURCES = [os.path.join(CSRC, "tara_abi.cu"), os.path.join(CSRC, "tara_pack.cpp"),
-           os.path.join(CSRC, "tara_host.cpp")]
+SOURCES = [os.path.join(CSRC, f) for f in
+           ("tara_abi.cu", "tara_layer.cu", "tara_pack.cpp", "tara_host.cpp")]
 HEADERS = [os.path.join(ROOT, "include", "tara_attn.h")] + [
     os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cuh", ".h"))]
 

@@ -1,0 +1,60 @@
+// linear_common.cuh -- arguments and epilogue arithmetic shared by the linear-layer kernels:
+//   y = residual + gate * act(x W^T + bias)
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace tara {
+
+// A strided [B][H][N][D] view whose rows are indexed by column c = h * D + d.
+struct RowView {
+  const void* ptr;
+  long long b, h, n;    // strides, elements
+  int D;
+};
+
+__device__ __forceinline__ long long row_offset(const RowView& v, int b, long long n, int col) {
+  const int h = col / v.D;
+  return b * v.b + h * v.h + n * v.n + (col - h * v.D);
+}
+
+struct LinearArgs {
+  RowView x, residual;      // residual.ptr == nullptr: none
+  RowView y[3];             // y[col / part_cols], column col % part_cols
+  int part_cols;            // C for one output; H*D for q, k, v
+  const void *w, *bias, *gate;
+  long long gate_b;         // elements between branches' gates
+  int act;
+  int B, N, K, C;           // N tokens a branch, K input columns, C output columns
+  int* status;
+};
+
+// Activations on the fp32 accumulator (numbering of tara_act).
+__device__ __forceinline__ float apply_act(float v, int act) {
+  if (act == 1) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  if (act == 2) {
+    // v/2 (1 + tanh u) = v / (1 + exp(-2u))
+    const float u = 0.79788456080286536f * (v + 0.044715f * v * v * v);
+    return __fdividef(v, 1.0f + __expf(-2.0f * u));
+  }
+  if (act == 3) return __fdividef(v, 1.0f + __expf(-v));
+  return v;
+}
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+}  // namespace tara

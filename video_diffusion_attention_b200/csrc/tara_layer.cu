@@ -1,0 +1,250 @@
+// tara_layer.cu -- C entry points of the operators around the attention: argument checks and
+// launches of the rotary table, the norm and rotation of Q and K, the linear layer and the
+// Q/K/V projection.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "tara_attn.h"
+#include "forward_internal.h"
+#include "layer_checks.h"
+#include "linear_simt.cuh"
+#include "norm_rope.cuh"
+
+namespace tara {
+namespace {
+
+int launched() { return cudaGetLastError() == cudaSuccess ? TARA_OK : TARA_ERR_CUDA; }
+
+// ---------------------------------------------------------------------------------------
+// norm and rotation
+// ---------------------------------------------------------------------------------------
+template <typename T, int LANES>
+int launch_norm_rope(const NormRopeArgs& a, int B, bool halves, cudaStream_t stream) {
+  const int rows = kNormRopeThreads / LANES;
+  const int slots = a.n_tensors * a.H;
+  const dim3 grid((unsigned)((a.N + (long long)rows - 1) / rows),
+                  (unsigned)((slots + a.slots_per_cta - 1) / a.slots_per_cta), (unsigned)B);
+  if (halves)
+    norm_rope_kernel<T, LANES, true><<<grid, kNormRopeThreads, 0, stream>>>(a);
+  else
+    norm_rope_kernel<T, LANES, false><<<grid, kNormRopeThreads, 0, stream>>>(a);
+  return launched();
+}
+
+template <typename T>
+int launch_norm_rope_t(const NormRopeArgs& a, int B, bool halves, cudaStream_t stream) {
+  if (a.D <= 64) return launch_norm_rope<T, 8>(a, B, halves, stream);
+  if (a.D <= 128) return launch_norm_rope<T, 16>(a, B, halves, stream);
+  return launch_norm_rope<T, 32>(a, B, halves, stream);
+}
+
+int run_norm_rope(const tara_view* q, const tara_view* k, const tara_norm_rope* p,
+                  const tara_view* q_out, const tara_view* k_out, cudaStream_t stream) {
+  NormRopeArgs a{};
+  const tara_view* in[2] = {q, k};
+  const tara_view* out[2] = {q_out, k_out};
+  const void* weight[2] = {p->q_weight, p->k_weight};
+  a.n_tensors = k ? 2 : 1;
+  for (int i = 0; i < a.n_tensors; ++i) {
+    const tara_view vi = normalised(*in[i]), vo = normalised(*out[i]);
+    a.t[i] = NormRopeTensor{vi.ptr, vo.ptr, weight[i], vi.stride_b, vi.stride_h, vi.stride_n,
+                            vo.stride_b, vo.stride_h, vo.stride_n};
+  }
+  a.table = p->table;
+  a.table_b = p->table_batch_stride;
+  a.weight_h = p->weight_head_stride;
+  a.H = q->H;
+  a.N = q->N;
+  a.D = q->D;
+  a.rot = p->table ? p->rot_dim : 0;
+  a.norm = p->norm;
+  a.eps = p->eps;
+  a.inv_d = 1.0f / (float)q->D;
+  a.slots_per_cta = 1;
+  const bool halves = p->pairing == TARA_ROPE_HALVES;
+  if (q->dtype == TARA_BF16) return launch_norm_rope_t<__nv_bfloat16>(a, q->B, halves, stream);
+  if (q->dtype == TARA_FP16) return launch_norm_rope_t<__half>(a, q->B, halves, stream);
+  return launch_norm_rope_t<float>(a, q->B, halves, stream);
+}
+
+// ---------------------------------------------------------------------------------------
+// linear
+// ---------------------------------------------------------------------------------------
+RowView row_view(const tara_view& v) {
+  const tara_view n = normalised(v);
+  return RowView{n.ptr, n.stride_b, n.stride_h, n.stride_n, n.D};
+}
+
+// A view of the linear layer: 16-bit views are read and written by 16-byte chunks and 64-column
+// boxes of the tensor maps; the fp32 kernel takes anything.
+int check_linear_view(const tara_view* v, bool out) {
+  if (!v) return TARA_ERR_NULL;
+  const int align = v->dtype == TARA_FP32 ? 0 : 16;
+  const int rc = out ? check_out_view(v, align) : check_view(v, align);
+  if (rc != TARA_OK) return rc;
+  if (v->dtype != TARA_FP32 && (v->D % 8 != 0 || (v->H > 1 && v->D % 64 != 0)))
+    return TARA_ERR_SHAPE;
+  return TARA_OK;
+}
+
+int run_linear(const LinearArgs& a, tara_dtype dt, cudaStream_t stream) {
+  const long long gx = ((long long)a.N + kSimtLinTile - 1) / kSimtLinTile;
+  const long long gy = ((long long)a.C + kSimtLinTile - 1) / kSimtLinTile;
+  if (gy > 65535) return TARA_ERR_TOO_LARGE;
+  const dim3 grid((unsigned)gx, (unsigned)gy, (unsigned)a.B);
+  if (dt == TARA_BF16)
+    linear_simt_kernel<__nv_bfloat16><<<grid, kSimtLinThreads, 0, stream>>>(a);
+  else if (dt == TARA_FP16)
+    linear_simt_kernel<__half><<<grid, kSimtLinThreads, 0, stream>>>(a);
+  else
+    linear_simt_kernel<float><<<grid, kSimtLinThreads, 0, stream>>>(a);
+  return launched();
+}
+
+// The whole per-token column count of a view.
+int64_t columns(const tara_view& v) { return (int64_t)v.H * v.D; }
+
+}  // namespace
+}  // namespace tara
+
+using namespace tara;
+
+extern "C" {
+
+int tara_rope_table(const float* pos, int64_t n_rows, const tara_rope* rope, float* table,
+                    void* stream) {
+  if (!pos || !rope || !table) return TARA_ERR_NULL;
+  if (rope->n_axes < 1 || rope->n_axes > TARA_ROPE_MAX_AXES) return TARA_ERR_PARAM;
+  if (n_rows < 1) return TARA_ERR_SHAPE;
+  int R = 0;
+  for (int a = 0; a < rope->n_axes; ++a) {
+    if (!(rope->theta[a] > 0.0) || !std::isfinite(rope->theta[a])) return TARA_ERR_PARAM;
+    if (rope->dim[a] < 2 || rope->dim[a] % 2 != 0 || rope->dim[a] > 2 * kRopeMaxPairs)
+      return TARA_ERR_SHAPE;
+    R += rope->dim[a];
+  }
+  if (R > 2 * kRopeMaxPairs || R % 4 != 0) return TARA_ERR_SHAPE;
+  if (!ptr_aligned(pos, 4) || !ptr_aligned(table, 16)) return TARA_ERR_ALIGN;
+  RopeFreqs fr{};
+  fr.n_axes = rope->n_axes;
+  for (int a = 0; a < rope->n_axes; ++a)
+    for (int i = 0; i < rope->dim[a] / 2; ++i) {
+      fr.axis[fr.n_pairs] = (uint8_t)a;
+      fr.quarter_turns[fr.n_pairs++] =
+          std::pow(rope->theta[a], -2.0 * i / rope->dim[a]) * 0.63661977236758134308;   // 2/pi
+    }
+  const long long total = (long long)n_rows * fr.n_pairs;
+  const long long grid = (total + kRopeThreads - 1) / kRopeThreads;
+  if (grid > 0x7fffffffLL) return TARA_ERR_TOO_LARGE;
+  rope_table_kernel<<<(unsigned)grid, kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+      pos, n_rows, fr, reinterpret_cast<float2*>(table));
+  return launched();
+}
+
+int tara_qk_norm_rope(const tara_view* q, const tara_view* k, const tara_norm_rope* p,
+                      tara_view* q_out, tara_view* k_out, void* stream) {
+  if (!q || !p || !q_out || (k == nullptr) != (k_out == nullptr)) return TARA_ERR_NULL;
+  int rc;
+  if ((rc = check_view(q, 16)) != TARA_OK || (rc = check_out_view(q_out, 16)) != TARA_OK)
+    return rc;
+  if (k && ((rc = check_view(k, 16)) != TARA_OK || (rc = check_out_view(k_out, 16)) != TARA_OK))
+    return rc;
+  const tara_view* all[4] = {q, q_out, k, k_out};
+  for (const tara_view* v : all) {
+    if (!v) continue;
+    if (v->dtype != q->dtype) return TARA_ERR_DTYPE;
+    if (!same_shape(*v, *q)) return TARA_ERR_SHAPE;
+  }
+  if (q->D % 8 != 0 || q->D > 256) return TARA_ERR_HEAD_DIM;
+  if (2LL * q->H > 65535) return TARA_ERR_TOO_LARGE;
+  if ((rc = check_norm_rope(p, q->H, q->D, q->N, q->dtype)) != TARA_OK) return rc;
+  // an output is its own input, or starts elsewhere than every other view
+  if (q_out->ptr == q->ptr && !same_layout(*q_out, *q)) return TARA_ERR_PARAM;
+  if (k) {
+    if (k_out->ptr == k->ptr && !same_layout(*k_out, *k)) return TARA_ERR_PARAM;
+    if (q_out->ptr == k->ptr || k_out->ptr == q->ptr || q_out->ptr == k_out->ptr)
+      return TARA_ERR_PARAM;
+  }
+  return run_norm_rope(q, k, p, q_out, k_out, static_cast<cudaStream_t>(stream));
+}
+
+int tara_linear(const tara_view* x, const void* w, const tara_epilogue* e, tara_view* y,
+                void* stream) {
+  if (!x || !w || !y) return TARA_ERR_NULL;
+  int rc;
+  if ((rc = check_linear_view(x, false)) != TARA_OK || (rc = check_linear_view(y, true)) != TARA_OK)
+    return rc;
+  if (x->dtype != y->dtype) return TARA_ERR_DTYPE;
+  if (x->B != y->B || x->N != y->N) return TARA_ERR_SHAPE;
+  const uintptr_t align = x->dtype == TARA_FP32 ? 4 : 16;
+  if (!ptr_aligned(w, align)) return TARA_ERR_ALIGN;
+  if (y->ptr == x->ptr || y->ptr == w) return TARA_ERR_PARAM;
+  LinearArgs a{};
+  a.x = row_view(*x);
+  a.y[0] = row_view(*y);
+  a.w = w;
+  a.B = x->B;
+  a.N = x->N;
+  a.K = (int)columns(*x);
+  a.C = (int)columns(*y);
+  a.part_cols = a.C;
+  if (e) {
+    if (e->act < TARA_ACT_NONE || e->act > TARA_ACT_SILU) return TARA_ERR_PARAM;
+    if (e->gate && e->gate_stride != 0 && e->gate_stride < a.C) return TARA_ERR_PARAM;
+    if (!ptr_aligned(e->bias, align) || !ptr_aligned(e->gate, align)) return TARA_ERR_ALIGN;
+    if (e->gate && (e->gate_stride * elem_size(x->dtype)) % (int)align != 0) return TARA_ERR_ALIGN;
+    a.bias = e->bias;
+    a.act = e->act;
+    a.gate = e->gate;
+    a.gate_b = e->gate_stride;
+    if (e->residual) {
+      const tara_view* r = e->residual;
+      if ((rc = check_linear_view(r, false)) != TARA_OK) return rc;
+      if (r->dtype != x->dtype) return TARA_ERR_DTYPE;
+      if (r->B != y->B || r->N != y->N || columns(*r) != columns(*y)) return TARA_ERR_SHAPE;
+      if (r->ptr == y->ptr && !same_layout(*r, *y)) return TARA_ERR_PARAM;
+      a.residual = row_view(*r);
+    }
+  }
+  return run_linear(a, x->dtype, static_cast<cudaStream_t>(stream));
+}
+
+int tara_qkv_project(const tara_view* x, const void* w, const void* bias,
+                     const tara_norm_rope* p, tara_view* q, tara_view* k, tara_view* v,
+                     void* stream) {
+  if (!x || !w || !q || !k || !v) return TARA_ERR_NULL;
+  int rc;
+  if ((rc = check_linear_view(x, false)) != TARA_OK) return rc;
+  const tara_view* outs[3] = {q, k, v};
+  for (const tara_view* o : outs) {
+    if ((rc = check_out_view(o, 16)) != TARA_OK) return rc;
+    if (o->dtype != x->dtype) return TARA_ERR_DTYPE;
+    if (!same_shape(*o, *q) || o->B != x->B || o->N != x->N) return TARA_ERR_SHAPE;
+    if (o->ptr == x->ptr || o->ptr == w) return TARA_ERR_PARAM;
+  }
+  if (q->ptr == k->ptr || q->ptr == v->ptr || k->ptr == v->ptr) return TARA_ERR_PARAM;
+  if (q->dtype == TARA_FP32 ? (q->D % 8 != 0 || q->D > 256) : (q->D != 64 && q->D != 128))
+    return TARA_ERR_HEAD_DIM;
+  if (2LL * q->H > 65535 || 3 * columns(*q) > 0x7fffffffLL) return TARA_ERR_TOO_LARGE;
+  const uintptr_t align = x->dtype == TARA_FP32 ? 4 : 16;
+  if (!ptr_aligned(w, align) || !ptr_aligned(bias, align)) return TARA_ERR_ALIGN;
+  if (p && (rc = check_norm_rope(p, q->H, q->D, q->N, q->dtype)) != TARA_OK) return rc;
+  LinearArgs a{};
+  a.x = row_view(*x);
+  for (int i = 0; i < 3; ++i) a.y[i] = row_view(*outs[i]);
+  a.w = w;
+  a.bias = bias;
+  a.B = x->B;
+  a.N = x->N;
+  a.K = (int)columns(*x);
+  a.part_cols = (int)columns(*q);
+  a.C = 3 * a.part_cols;
+  if ((rc = run_linear(a, x->dtype, static_cast<cudaStream_t>(stream))) != TARA_OK || !p) return rc;
+  return run_norm_rope(q, k, p, q, k, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -73,4 +73,36 @@ int tara_pack_token_meta(const tara_segment* segs, int32_t n_segs, uint8_t* seg,
   return TARA_OK;
 }
 
+int tara_pack_token_positions(const tara_grid* grids, int32_t n_grids, int32_t n_axes,
+                              float* pos, int64_t N) {
+  if (n_axes < 1 || n_axes > TARA_ROPE_MAX_AXES) return TARA_ERR_PARAM;
+  if (n_grids < 0) return TARA_ERR_SEGMENT;
+  if (n_grids > 0 && grids == nullptr) return TARA_ERR_NULL;
+  int64_t total = 0;
+  for (int32_t g = 0; g < n_grids; ++g) {
+    const tara_grid& t = grids[g];
+    if (t.frames < 1 || t.rows < 1 || t.cols < 1) return TARA_ERR_SEGMENT;
+    for (int32_t a = 0; a < n_axes; ++a)
+      if (!std::isfinite(t.origin[a]) || !std::isfinite(t.frame_step[a]) ||
+          !std::isfinite(t.row_step[a]) || !std::isfinite(t.col_step[a]))
+        return TARA_ERR_SEGMENT;
+    // counted without overflow: a grid longer than N (or a sum past it) cannot match
+    const int64_t plane = (int64_t)t.rows * t.cols;
+    if (plane > N || t.frames > (N - total) / plane) return TARA_ERR_CAPACITY;
+    total += plane * t.frames;
+  }
+  if (total != N) return TARA_ERR_CAPACITY;
+  if (N > 0 && pos == nullptr) return TARA_ERR_NULL;
+  for (int32_t g = 0; g < n_grids; ++g) {
+    const tara_grid& t = grids[g];
+    for (int32_t f = 0; f < t.frames; ++f)
+      for (int32_t r = 0; r < t.rows; ++r)
+        for (int32_t c = 0; c < t.cols; ++c)
+          for (int32_t a = 0; a < n_axes; ++a)
+            *pos++ = (float)(t.origin[a] + f * t.frame_step[a] + r * t.row_step[a] +
+                             c * t.col_step[a]);
+  }
+  return TARA_OK;
+}
+
 }  // extern "C"
