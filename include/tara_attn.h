@@ -454,8 +454,8 @@ int tara_linear(const tara_view* x, const void* w, const tara_epilogue* e, tara_
  * rows of the packed tensors tara_attn_forward takes).
  *   w : device [3*H*D][C_in]: the rows of q's heads, then k's, then v's.  bias [3*H*D] or NULL.
  *   p : NULL: no norm and no rotation.
- * bf16/fp16: D = 64 or 128.
- * fp32: D as in tara_qk_norm_rope.  Other requirements and errors as for
+ * bf16/fp16: D = 64 or 128; one kernel, the norm on the fp32 accumulators, one rounding.
+ * fp32: D as in tara_qk_norm_rope, two kernels.  Other requirements and errors as for
  * tara_linear and tara_qk_norm_rope.                                                       */
 int tara_qkv_project(const tara_view* x, const void* w, const void* bias,
                      const tara_norm_rope* p, tara_view* q, tara_view* k, tara_view* v,

@@ -286,6 +286,16 @@ QKV_CASES = [
     # B, N, K, H, D, dtype, heads of x, bias, norm, weight, dims, halves
     (1, 40, 72, 2, 24, "fp32", 0, True, True, "shared", (8, 16), False),
     (2, 9, 128, 3, 64, "fp32", 2, False, True, "head", (16, 24, 24), True),
+    (1, 1, 128, 2, 128, "bf16", 0, True, True, "shared", (16, 56, 56), False),
+    (2, 1, 72, 3, 64, "fp16", 0, True, True, "head", (64,), True),
+    (3, 7, 264, 1, 128, "bf16", 0, False, True, None, (16, 16), True),
+    (1, 33, 200, 5, 64, "bf16", 0, True, False, None, (24, 20, 20), False),
+    (1, 128, 256, 2, 128, "fp16", 2, True, True, "shared", None, False),
+    (1, 100, 256, 2, 128, "fp16", 0, True, False, None, None, False),      # neither: plain products
+    (2, 300, 320, 4, 128, "bf16", 5, True, True, "head", (16, 56, 56), True),
+    (1, 700, 512, 7, 64, "fp16", 0, True, True, "shared", (16, 16), True),
+    (1, 1030, 136, 6, 128, "bf16", 0, True, True, "shared", (44, 42, 42), False),
+    (2, 515, 192, 9, 64, "bf16", 0, False, True, "head", (24, 20, 20), False),
 ]
 
 

@@ -8,6 +8,17 @@
 
 namespace tara {
 
+// What the kernels of every translation unit share on the current device: its status word
+// (tara_device_status), its number of SMs, its index, and the driver's tensor-map encoder (an
+// address of cuTensorMapEncodeTiled, resolved once per process).
+struct DeviceInfo {
+  int* status;
+  int sms;
+  int index;
+  void* encode_tiled;
+};
+int device_info(DeviceInfo* out);
+
 // Device workspace one tara_attn_forward call of this shape needs: the tile and per-key records
 // of every metadata set and, with qk_int8, the 8-bit copies of Q and K and their scales.  0 for
 // fp32 tensors (the CUDA-core kernel reads the metadata directly).

@@ -484,6 +484,21 @@ int forward_locked(const tara_tensor* Q, const tara_tensor* K, const tara_tensor
 
 }  // namespace
 
+int device_info(DeviceInfo* out) {
+  static int sms[kMaxDevices];   // 0: not looked up yet (guarded by g_mu)
+  int rc = get_encode_fn();
+  if (rc != TARA_OK) return rc;
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* st = nullptr;
+  if ((rc = device_state(0, &st)) != TARA_OK) return rc;
+  const int dev = (int)(st - g_dev);
+  if (sms[dev] == 0 &&
+      cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return TARA_ERR_CUDA;
+  *out = DeviceInfo{st->status, sms[dev], dev, reinterpret_cast<void*>(g_encode)};
+  return TARA_OK;
+}
+
 size_t forward_workspace_bytes(const tara_tensor* Q, const tara_token_meta* meta,
                                const tara_params* p) {
   return ws_layout(Q, meta, p).total;

@@ -7,10 +7,12 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "tara_attn.h"
 #include "forward_internal.h"
 #include "layer_checks.h"
+#include "linear_pair.cuh"
 #include "linear_simt.cuh"
 #include "norm_rope.cuh"
 
@@ -91,18 +93,135 @@ int check_linear_view(const tara_view* v, bool out) {
   return TARA_OK;
 }
 
-int run_linear(const LinearArgs& a, tara_dtype dt, cudaStream_t stream) {
-  const long long gx = ((long long)a.N + kSimtLinTile - 1) / kSimtLinTile;
-  const long long gy = ((long long)a.C + kSimtLinTile - 1) / kSimtLinTile;
-  if (gy > 65535) return TARA_ERR_TOO_LARGE;
-  const dim3 grid((unsigned)gx, (unsigned)gy, (unsigned)a.B);
-  if (dt == TARA_BF16)
-    linear_simt_kernel<__nv_bfloat16><<<grid, kSimtLinThreads, 0, stream>>>(a);
-  else if (dt == TARA_FP16)
-    linear_simt_kernel<__half><<<grid, kSimtLinThreads, 0, stream>>>(a);
-  else
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Tensor map of a row-major 16-bit array of up to 4 dimensions (innermost first; strides of
+// dimensions 1.. in elements): 128-byte-swizzled boxes of 64 columns x box_rows.
+int encode_map(const DeviceInfo& dev, CUtensorMap* map, tara_dtype dt, const void* ptr, int rank,
+               const long long* dims, const long long* strides, int box_rows) {
+  cuuint64_t gdim[4], gstr[3];
+  cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1}, estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) gdim[i] = (cuuint64_t)dims[i];
+  // the stride of a dimension of size 1 is never used, but has to be a valid one
+  for (int i = 1; i < rank; ++i)
+    gstr[i - 1] = dims[i] == 1 ? (cuuint64_t)((dims[0] + 7) / 8 * 16) : (cuuint64_t)strides[i] * 2;
+  const CUresult r = reinterpret_cast<EncodeTiledFn>(dev.encode_tiled)(
+      map, dt == TARA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+      (cuuint32_t)rank, const_cast<void*>(ptr), gdim, gstr, box, estr,
+      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? TARA_OK : TARA_ERR_CUDA;
+}
+
+// [B][H][N][D] view with `cols` columns of rows in all.
+int encode_view(const DeviceInfo& dev, CUtensorMap* map, tara_dtype dt, const RowView& v, int B,
+                int N, int cols, int box_rows) {
+  const long long dims[4] = {v.D, N, cols / v.D, B}, strides[4] = {1, v.n, v.h, v.b};
+  return encode_map(dev, map, dt, v.ptr, 4, dims, strides, box_rows);
+}
+
+int encode_weights(const DeviceInfo& dev, CUtensorMap* map, tara_dtype dt, const void* w, int C,
+                   int K, int box_rows) {
+  const long long dims[2] = {K, C}, strides[2] = {1, K};
+  return encode_map(dev, map, dt, w, 2, dims, strides, box_rows);
+}
+
+template <bool kBF16, int BN, bool kQkv>
+struct PairLauncher {
+  static int allow(const DeviceInfo& dev) {
+    static std::mutex mu;
+    static uint64_t done = 0;   // one bit per device
+    std::lock_guard<std::mutex> lock(mu);
+    if (done >> dev.index & 1) return TARA_OK;
+    if (cudaFuncSetAttribute(linear_pair_kernel<kBF16, BN, kQkv>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             PairLin<BN>::kSmemBytes) != cudaSuccess)
+      return TARA_ERR_CUDA;
+    done |= (uint64_t)1 << dev.index;
+    return TARA_OK;
+  }
+  static int launch(const DeviceInfo& dev, const PairLinArgs& args, tara_dtype dt,
+                    cudaStream_t stream) {
+    int rc;
+    if ((rc = allow(dev)) != TARA_OK) return rc;
+    const LinearArgs& a = args.lin;
+    PairLinArgs p = args;
+    PairLinMaps maps;
+    if ((rc = encode_view(dev, &maps.x, dt, a.x, a.B, a.N, a.K, 128)) != TARA_OK ||
+        (rc = encode_weights(dev, &maps.w, dt, a.w, a.C, a.K, BN / 2)) != TARA_OK)
+      return rc;
+    const int parts = a.C / a.part_cols;
+    for (int i = 0; i < 3; ++i) {
+      const RowView& y = a.y[i < parts ? i : 0];
+      if ((rc = encode_view(dev, &maps.y[i], dt, y, a.B, a.N, a.part_cols, 32)) != TARA_OK) return rc;
+    }
+    p.m_tiles = (int)(((long long)a.N + 255) / 256);
+    p.n_tiles = (int)(((long long)a.C + BN - 1) / BN);
+    p.group = 8;
+    const long long tiles = (long long)a.B * p.m_tiles * p.n_tiles;
+    const long long clusters = std::min<long long>(tiles, std::max(1, dev.sms / 2));
+    linear_pair_kernel<kBF16, BN, kQkv>
+        <<<(unsigned)(2 * clusters), kPairLinThreads, PairLin<BN>::kSmemBytes, stream>>>(maps, p);
+    return launched();
+  }
+};
+
+// Folds the branches into one run of rows where every view allows it and nothing is per branch.
+void merge_branches(LinearArgs* a) {
+  if (a->B == 1 || a->gate_b != 0 || (long long)a->B * a->N > 0x7fffffffLL) return;
+  auto runs_on = [a](const RowView& v) { return a->N == 1 ? true : v.b == v.n * a->N; };
+  const int parts = a->C / a->part_cols;
+  if (!runs_on(a->x) || (a->residual.ptr && !runs_on(a->residual))) return;
+  for (int i = 0; i < parts; ++i)
+    if (!runs_on(a->y[i])) return;
+  if (a->N == 1) {
+    a->x.n = a->x.b;
+    a->residual.n = a->residual.b;
+    for (int i = 0; i < parts; ++i) a->y[i].n = a->y[i].b;
+  }
+  a->N *= a->B;
+  a->B = 1;
+}
+
+template <bool kBF16, int BN>
+int launch_pair(const DeviceInfo& dev, const PairLinArgs& p, bool heads, tara_dtype dt,
+                cudaStream_t stream) {
+  return heads ? PairLauncher<kBF16, BN, true>::launch(dev, p, dt, stream)
+               : PairLauncher<kBF16, BN, false>::launch(dev, p, dt, stream);
+}
+
+// head: the norm and rotation of a projection's q and k, or nullptr.
+int run_linear(LinearArgs a, const HeadArgs* head, tara_dtype dt, cudaStream_t stream) {
+  if (dt == TARA_FP32) {
+    const long long gx = ((long long)a.N + kSimtLinTile - 1) / kSimtLinTile;
+    const long long gy = ((long long)a.C + kSimtLinTile - 1) / kSimtLinTile;
+    if (gy > 65535) return TARA_ERR_TOO_LARGE;
+    const dim3 grid((unsigned)gx, (unsigned)gy, (unsigned)a.B);
     linear_simt_kernel<float><<<grid, kSimtLinThreads, 0, stream>>>(a);
-  return launched();
+    return launched();
+  }
+  DeviceInfo dev;
+  int rc = device_info(&dev);
+  if (rc != TARA_OK) return rc;
+  a.status = dev.status;
+  if (!head || !head->table) merge_branches(&a);
+  // the kernel numbers its tiles in int
+  const long long tiles128 = (long long)a.B * (((long long)a.N + 255) / 256) *
+                             (((long long)a.C + 127) / 128);
+  if (tiles128 > 0x3fffffffLL) return TARA_ERR_TOO_LARGE;
+  PairLinArgs p{};
+  p.lin = a;
+  if (head) p.head = *head;
+  // 256 columns a tile halve the loads of x per product; 128 where 256 would leave SM pairs idle
+  const bool wide = tiles128 / 2 >= dev.sms / 2;
+  if (dt == TARA_BF16)
+    return wide ? launch_pair<true, 256>(dev, p, head != nullptr, dt, stream)
+                : launch_pair<true, 128>(dev, p, head != nullptr, dt, stream);
+  return wide ? launch_pair<false, 256>(dev, p, head != nullptr, dt, stream)
+              : launch_pair<false, 128>(dev, p, head != nullptr, dt, stream);
 }
 
 // The whole per-token column count of a view.
@@ -210,7 +329,7 @@ int tara_linear(const tara_view* x, const void* w, const tara_epilogue* e, tara_
       a.residual = row_view(*r);
     }
   }
-  return run_linear(a, x->dtype, static_cast<cudaStream_t>(stream));
+  return run_linear(a, nullptr, x->dtype, static_cast<cudaStream_t>(stream));
 }
 
 int tara_qkv_project(const tara_view* x, const void* w, const void* bias,
@@ -243,8 +362,26 @@ int tara_qkv_project(const tara_view* x, const void* w, const void* bias,
   a.K = (int)columns(*x);
   a.part_cols = (int)columns(*q);
   a.C = 3 * a.part_cols;
-  if ((rc = run_linear(a, x->dtype, static_cast<cudaStream_t>(stream))) != TARA_OK || !p) return rc;
-  return run_norm_rope(q, k, p, q, k, static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (x->dtype == TARA_FP32) {
+    if ((rc = run_linear(a, nullptr, x->dtype, st)) != TARA_OK || !p) return rc;
+    return run_norm_rope(q, k, p, q, k, st);
+  }
+  HeadArgs head{};
+  if (p) {
+    head.weight[0] = p->norm ? p->q_weight : nullptr;
+    head.weight[1] = p->norm ? p->k_weight : nullptr;
+    head.weight_h = p->weight_head_stride;
+    head.table = p->table;
+    head.table_b = p->table_batch_stride;
+    head.D = q->D;
+    head.rot = p->table ? p->rot_dim : 0;
+    head.halves = p->pairing == TARA_ROPE_HALVES;
+    head.norm = p->norm;
+    head.eps = p->eps;
+    head.inv_d = 1.0f / (float)q->D;
+  }
+  return run_linear(a, p ? &head : nullptr, x->dtype, st);
 }
 
 }  // extern "C"
