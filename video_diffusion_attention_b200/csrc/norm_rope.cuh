@@ -123,6 +123,9 @@ rope_table_kernel(const float* __restrict__ pos, long long n_rows,
 // ---------------------------------------------------------------------------------------
 // norm_rope_kernel: a row of one head lies across LANES lanes, 8 elements a lane
 // ---------------------------------------------------------------------------------------
+// HBM-bound: every element of q and k is read and written once, ~10 operations each.  A warp
+// keeps 32/LANES tokens and walks heads, so a token's (cos, sin) pairs are read once for all
+// the heads of a CTA and stay in registers, and kBatch heads' loads are in flight per lane.
 struct NormRopeTensor {
   const void* in;
   void* out;
@@ -135,10 +138,10 @@ struct NormRopeArgs {
   const float* table;
   long long table_b;       // floats between branches' tables
   long long weight_h;      // elements between heads' weights (0: shared)
-  int n_tensors, H, N, D, rot;
+  int H, N, D, rot;
   int norm;
   float eps, inv_d;
-  int slots_per_cta;       // (tensor, head) slots one CTA walks
+  int heads_per_cta, chunks;   // blockIdx.y = tensor * chunks + chunk of heads_per_cta heads
 };
 
 constexpr int kNormRopeThreads = 256;
@@ -147,6 +150,7 @@ template <typename T, int LANES, bool kHalves>
 __global__ void __launch_bounds__(kNormRopeThreads)
 norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   constexpr int kRows = 32 / LANES;                       // token rows per warp
+  constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;          // heads in flight
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int l = lane % LANES;
   const long long n =
@@ -168,57 +172,68 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
       cs[4 * i] = v.x; cs[4 * i + 1] = v.y; cs[4 * i + 2] = v.z; cs[4 * i + 3] = v.w;
     }
   }
+  // the other half of each pair lies rot/16 lanes away in the same row
+  const int partner = (lane - l) + (l < half ? l + half : (l < 2 * half ? l - half : l));
+  const float sign = l < half ? -1.f : 1.f;
 
-  const int s_begin = blockIdx.y * a.slots_per_cta;
-  const int s_end = min(s_begin + a.slots_per_cta, a.n_tensors * a.H);
-  for (int s = s_begin; s < s_end; ++s) {
-    const NormRopeTensor& t = a.t[s >= a.H ? 1 : 0];
-    const int h = s >= a.H ? s - a.H : s;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (live) {
-      Vec8<T> v;
-      v.load(static_cast<const T*>(t.in) + b * t.in_b + h * t.in_h + n * t.in_n + 8 * l);
-      v.unpack(x);
-    }
-    if (a.norm) {
-      float ss = 0.f;
+  const int which = blockIdx.y / a.chunks;
+  const NormRopeTensor& t = a.t[which];
+  const int h0 = (blockIdx.y - which * a.chunks) * a.heads_per_cta;
+  const int h1 = min(h0 + a.heads_per_cta, a.H);
+  const T* in = static_cast<const T*>(t.in) + b * t.in_b + n * t.in_n + 8 * l;
+  T* out = static_cast<T*>(t.out) + b * t.out_b + n * t.out_n + 8 * l;
+  const T* weight = static_cast<const T*>(t.weight) + 8 * l;
+  const bool weighted = a.norm && t.weight != nullptr && live;
+  float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+  if (weighted) {
+    Vec8<T> wv;
+    wv.load(weight);
+    wv.unpack(w);
+  }
+
+  for (int h = h0; h < h1; h += kBatch) {
+    Vec8<T> v[kBatch];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+    for (int i = 0; i < kBatch; ++i)
+      if (live && h + i < h1) v[i].load(in + (h + i) * t.in_h);
 #pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float r = __frsqrt_rn(fmaf(ss, a.inv_d, a.eps));
+    for (int i = 0; i < kBatch; ++i) {
+      if (h + i >= h1) break;                             // the same for the whole warp
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (live) v[i].unpack(x);
+      if (a.norm) {
+        float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= r;
-      if (t.weight != nullptr && live) {
-        Vec8<T> wv;
-        float w[8];
-        wv.load(static_cast<const T*>(t.weight) + h * a.weight_h + 8 * l);
-        wv.unpack(w);
+        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= w[i];
-      }
-    }
-    if (a.table != nullptr) {
-      if (kHalves) {
-        // the other half of each pair lies rot/16 lanes away in the same row
-        const int partner = (lane - l) + (l < half ? l + half : (l < 2 * half ? l - half : l));
-        const float sign = l < half ? -1.f : 1.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float y = __shfl_sync(0xffffffffu, x[i], partner);
-          if (turned) x[i] = fmaf(x[i], cs[2 * i], sign * y * cs[2 * i + 1]);
+        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = __frsqrt_rn(fmaf(ss, a.inv_d, a.eps));
+        if (a.weight_h != 0 && weighted) {
+          Vec8<T> wv;
+          wv.load(weight + (h + i) * a.weight_h);
+          wv.unpack(w);
         }
-      } else if (turned) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float u = x[2 * i], w = x[2 * i + 1], c = cs[2 * i], sn = cs[2 * i + 1];
-          x[2 * i] = fmaf(u, c, -w * sn);
-          x[2 * i + 1] = fmaf(u, sn, w * c);
+        for (int j = 0; j < 8; ++j) x[j] *= r * w[j];
+      }
+      if (a.table != nullptr) {
+        if (kHalves) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float y = __shfl_sync(0xffffffffu, x[j], partner);
+            if (turned) x[j] = fmaf(x[j], cs[2 * j], sign * y * cs[2 * j + 1]);
+          }
+        } else if (turned) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float u = x[2 * j], z = x[2 * j + 1], c = cs[2 * j], sn = cs[2 * j + 1];
+            x[2 * j] = fmaf(u, c, -z * sn);
+            x[2 * j + 1] = fmaf(u, sn, z * c);
+          }
         }
       }
+      if (live) Vec8<T>::store(out + (h + i) * t.out_h, x);
     }
-    if (live)
-      Vec8<T>::store(static_cast<T*>(t.out) + b * t.out_b + h * t.out_h + n * t.out_n + 8 * l, x);
   }
 }
 

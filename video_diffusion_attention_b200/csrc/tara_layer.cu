@@ -24,12 +24,19 @@ int launched() { return cudaGetLastError() == cudaSuccess ? TARA_OK : TARA_ERR_C
 // ---------------------------------------------------------------------------------------
 // norm and rotation
 // ---------------------------------------------------------------------------------------
+// CTAs that keep every SM of the device busy through a few rounds.
+constexpr long long kNormRopeFill = 148 * 16;
+
 template <typename T, int LANES>
-int launch_norm_rope(const NormRopeArgs& a, int B, bool halves, cudaStream_t stream) {
+int launch_norm_rope(NormRopeArgs a, int B, int n_tensors, bool halves, cudaStream_t stream) {
   const int rows = kNormRopeThreads / LANES;
-  const int slots = a.n_tensors * a.H;
-  const dim3 grid((unsigned)((a.N + (long long)rows - 1) / rows),
-                  (unsigned)((slots + a.slots_per_cta - 1) / a.slots_per_cta), (unsigned)B);
+  const long long gx = ((long long)a.N + rows - 1) / rows;
+  // one CTA walks as many heads as leave the device a few CTAs per SM (the table is read once
+  // per CTA and token), at least one batch
+  const long long want = (kNormRopeFill + gx * B * n_tensors - 1) / (gx * B * n_tensors);
+  a.heads_per_cta = (int)std::max<long long>(4, (a.H + want - 1) / want);
+  a.chunks = (a.H + a.heads_per_cta - 1) / a.heads_per_cta;
+  const dim3 grid((unsigned)gx, (unsigned)(n_tensors * a.chunks), (unsigned)B);
   if (halves)
     norm_rope_kernel<T, LANES, true><<<grid, kNormRopeThreads, 0, stream>>>(a);
   else
@@ -38,10 +45,10 @@ int launch_norm_rope(const NormRopeArgs& a, int B, bool halves, cudaStream_t str
 }
 
 template <typename T>
-int launch_norm_rope_t(const NormRopeArgs& a, int B, bool halves, cudaStream_t stream) {
-  if (a.D <= 64) return launch_norm_rope<T, 8>(a, B, halves, stream);
-  if (a.D <= 128) return launch_norm_rope<T, 16>(a, B, halves, stream);
-  return launch_norm_rope<T, 32>(a, B, halves, stream);
+int launch_norm_rope_t(const NormRopeArgs& a, int B, int nt, bool halves, cudaStream_t stream) {
+  if (a.D <= 64) return launch_norm_rope<T, 8>(a, B, nt, halves, stream);
+  if (a.D <= 128) return launch_norm_rope<T, 16>(a, B, nt, halves, stream);
+  return launch_norm_rope<T, 32>(a, B, nt, halves, stream);
 }
 
 int run_norm_rope(const tara_view* q, const tara_view* k, const tara_norm_rope* p,
@@ -50,8 +57,8 @@ int run_norm_rope(const tara_view* q, const tara_view* k, const tara_norm_rope* 
   const tara_view* in[2] = {q, k};
   const tara_view* out[2] = {q_out, k_out};
   const void* weight[2] = {p->q_weight, p->k_weight};
-  a.n_tensors = k ? 2 : 1;
-  for (int i = 0; i < a.n_tensors; ++i) {
+  const int nt = k ? 2 : 1;
+  for (int i = 0; i < nt; ++i) {
     const tara_view vi = normalised(*in[i]), vo = normalised(*out[i]);
     a.t[i] = NormRopeTensor{vi.ptr, vo.ptr, weight[i], vi.stride_b, vi.stride_h, vi.stride_n,
                             vo.stride_b, vo.stride_h, vo.stride_n};
@@ -66,11 +73,10 @@ int run_norm_rope(const tara_view* q, const tara_view* k, const tara_norm_rope* 
   a.norm = p->norm;
   a.eps = p->eps;
   a.inv_d = 1.0f / (float)q->D;
-  a.slots_per_cta = 1;
   const bool halves = p->pairing == TARA_ROPE_HALVES;
-  if (q->dtype == TARA_BF16) return launch_norm_rope_t<__nv_bfloat16>(a, q->B, halves, stream);
-  if (q->dtype == TARA_FP16) return launch_norm_rope_t<__half>(a, q->B, halves, stream);
-  return launch_norm_rope_t<float>(a, q->B, halves, stream);
+  if (q->dtype == TARA_BF16) return launch_norm_rope_t<__nv_bfloat16>(a, q->B, nt, halves, stream);
+  if (q->dtype == TARA_FP16) return launch_norm_rope_t<__half>(a, q->B, nt, halves, stream);
+  return launch_norm_rope_t<float>(a, q->B, nt, halves, stream);
 }
 
 // ---------------------------------------------------------------------------------------
