@@ -6,10 +6,12 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "sm100_ptx.cuh"
+
 namespace tara {
 
 // ---------------------------------------------------------------------------------------
-// 8 consecutive elements of one row, as fp32
+// 8 elements of one row, as fp32: consecutive, or two groups of 4
 // ---------------------------------------------------------------------------------------
 template <typename T>
 struct Vec8;
@@ -20,6 +22,10 @@ struct Vec8<__nv_bfloat16> {
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     v = *reinterpret_cast<const uint4*>(p);
   }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, const __nv_bfloat16* q) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(q);
+    v = make_uint4(a.x, a.y, b.x, b.y);
+  }
   __device__ __forceinline__ void unpack(float (&f)[8]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -28,14 +34,22 @@ struct Vec8<__nv_bfloat16> {
       f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
+    *reinterpret_cast<uint4*>(p) = pack(f);
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, __nv_bfloat16* q, const float (&f)[8]) {
+    const uint4 v = pack(f);
+    *reinterpret_cast<uint2*>(p) = make_uint2(v.x, v.y);
+    *reinterpret_cast<uint2*>(q) = make_uint2(v.z, v.w);
   }
 };
 
@@ -44,6 +58,10 @@ struct Vec8<__half> {
   uint4 v;
   __device__ __forceinline__ void load(const __half* p) {
     v = *reinterpret_cast<const uint4*>(p);
+  }
+  __device__ __forceinline__ void load(const __half* p, const __half* q) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(q);
+    v = make_uint4(a.x, a.y, b.x, b.y);
   }
   __device__ __forceinline__ void unpack(float (&f)[8]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -54,36 +72,48 @@ struct Vec8<__half> {
       f[2 * i + 1] = t.y;
     }
   }
-  static __device__ __forceinline__ void store(__half* p, const float (&f)[8]) {
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  static __device__ __forceinline__ void store(__half* p, const float (&f)[8]) {
+    *reinterpret_cast<uint4*>(p) = pack(f);
+  }
+  static __device__ __forceinline__ void store(__half* p, __half* q, const float (&f)[8]) {
+    const uint4 v = pack(f);
+    *reinterpret_cast<uint2*>(p) = make_uint2(v.x, v.y);
+    *reinterpret_cast<uint2*>(q) = make_uint2(v.z, v.w);
   }
 };
 
 template <>
 struct Vec8<float> {
   float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+  __device__ __forceinline__ void load(const float* p) { load(p, p + 4); }
+  __device__ __forceinline__ void load(const float* p, const float* q) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(q);
   }
   __device__ __forceinline__ void unpack(float (&f)[8]) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   }
   static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    store(p, p + 4, f);
+  }
+  static __device__ __forceinline__ void store(float* p, float* q, const float (&f)[8]) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(q) = make_float4(f[4], f[5], f[6], f[7]);
   }
 };
 
 // ---------------------------------------------------------------------------------------
-// rope_table_kernel: one thread per (row, pair)
+// rope_table_kernel
 // ---------------------------------------------------------------------------------------
 constexpr int kRopeMaxPairs = 128;
 constexpr int kRopeThreads = 256;
@@ -96,28 +126,73 @@ struct RopeFreqs {
   int n_pairs, n_axes;
 };
 
-// cos and sin of `turns` quarter turns.  The whole quarter turns come off in double precision,
-// so the fp32 part sees at most an eighth of a turn either way and keeps an absolute error near
-// 2^-26 however far the position is.
-__device__ __forceinline__ float2 cos_sin_quarter_turns(double turns) {
-  const double whole = rint(turns);
-  float s, c;
-  sincospif(0.5f * (float)(turns - whole), &s, &c);
-  const int q = (int)((long long)whole & 3);
-  const float a = (q & 1) ? s : c, b = (q & 1) ? c : s;
-  return make_float2((q == 1 || q == 2) ? -a : a, (q >= 2) ? -b : b);
+// Angle p * f quarter turns -> the nearest whole number of quarter turns (its low bits) and the
+// remainder in radians, |remainder| <= pi/4.  Adding 1.5 * 2^52 rounds to a whole number whose
+// low bits are those of the sum; the fma forms the remainder without a second rounding of the
+// product, so the phase of far positions survives (|p * f| < 2^31).
+__device__ __forceinline__ float quarter_turn_remainder(double p, double f, int& quarter) {
+  const double magic = 6755399441055744.0;
+  const double m = fma(p, f, magic);
+  quarter = __double2loint(m);
+  return (float)(fma(p, f, -(m - magic)) * 1.5707963267948966);
 }
 
+// sin and cos of two angles |x| <= pi/4 by their Taylor series to x^9 and x^10 (the first terms
+// left out are below 2e-9 and 2e-10), two lanes at once in packed fp32.
+__device__ __forceinline__ void sin_cos_small2(float x0, float x1, float2 (&sc)[2]) {
+  auto both = [](float c) { return f32x2_pack(c, c); };
+  const uint64_t x = f32x2_pack(x0, x1);
+  const uint64_t zero = both(0.f);
+  const uint64_t y = f32x2_fma(x, x, zero);
+  uint64_t s = f32x2_fma(y, both(1.f / 362880.f), both(-1.f / 5040.f));
+  s = f32x2_fma(y, s, both(1.f / 120.f));
+  s = f32x2_fma(y, s, both(-1.f / 6.f));
+  s = f32x2_fma(f32x2_fma(x, y, zero), s, x);
+  uint64_t c = f32x2_fma(y, both(-1.f / 3628800.f), both(1.f / 40320.f));
+  c = f32x2_fma(y, c, both(-1.f / 720.f));
+  c = f32x2_fma(y, c, both(1.f / 24.f));
+  c = f32x2_fma(y, c, both(-0.5f));
+  c = f32x2_fma(y, c, both(1.f));
+  f32x2_unpack(s, sc[0].x, sc[1].x);
+  f32x2_unpack(c, sc[0].y, sc[1].y);
+}
+
+// (cos, sin) of an angle from its whole quarter turns and (sin, cos) of its remainder.
+__device__ __forceinline__ float2 turn_quarters(float2 sc, int q) {
+  const float a = (q & 1) ? sc.x : sc.y, b = (q & 1) ? sc.y : sc.x;
+  const uint32_t flip_cos = (uint32_t)(q + 1) << 30 & 0x80000000u;    // quarters 1 and 2
+  const uint32_t flip_sin = (uint32_t)q << 30 & 0x80000000u;          // quarters 2 and 3
+  return make_float2(__uint_as_float(__float_as_uint(a) ^ flip_cos),
+                     __uint_as_float(__float_as_uint(b) ^ flip_sin));
+}
+
+// Write-bound (8 bytes a pair).  A thread keeps two neighbouring pairs (one 16-byte store) and
+// walks kSteps rows, so pair index, axis and frequency are set up once; the positions of a
+// CTA's rows are read through L1.
+template <int kSteps>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_table_kernel(const float* __restrict__ pos, long long n_rows,
-                  const __grid_constant__ RopeFreqs fr, float2* __restrict__ table) {
-  const long long total = n_rows * fr.n_pairs;
-  const long long i = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
-  if (i >= total) return;
-  const long long row = i / fr.n_pairs;
-  const int j = (int)(i - row * fr.n_pairs);
-  const double p = (double)pos[row * fr.n_axes + fr.axis[j]];
-  table[i] = cos_sin_quarter_turns(p * fr.quarter_turns[j]);
+                  const __grid_constant__ RopeFreqs fr, float4* __restrict__ table) {
+  const int row_units = fr.n_pairs / 2;                   // 16-byte units of a row
+  const int rows_step = kRopeThreads / row_units;         // rows of one step
+  const int r = threadIdx.x / row_units, u = threadIdx.x - r * row_units;
+  if (r >= rows_step) return;
+  const double f0 = fr.quarter_turns[2 * u], f1 = fr.quarter_turns[2 * u + 1];
+  const int a0 = fr.axis[2 * u], a1 = fr.axis[2 * u + 1];
+  const long long row0 = (long long)blockIdx.x * rows_step * kSteps + r;
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const long long row = row0 + (long long)i * rows_step;
+    if (row >= n_rows) return;
+    const float* p = pos + row * fr.n_axes;
+    int q0, q1;
+    const float x0 = quarter_turn_remainder((double)p[a0], f0, q0);
+    const float x1 = quarter_turn_remainder((double)p[a1], f1, q1);
+    float2 sc[2];
+    sin_cos_small2(x0, x1, sc);
+    const float2 t0 = turn_quarters(sc[0], q0), t1 = turn_quarters(sc[1], q1);
+    table[row * row_units + u] = make_float4(t0.x, t0.y, t1.x, t1.y);
+  }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -126,6 +201,12 @@ rope_table_kernel(const float* __restrict__ pos, long long n_rows,
 // HBM-bound: every element of q and k is read and written once, ~10 operations each.  A warp
 // keeps 32/LANES tokens and walks heads, so a token's (cos, sin) pairs are read once for all
 // the heads of a CTA and stay in registers, and kBatch heads' loads are in flight per lane.
+//
+// Which 8 columns a lane holds: with interleaved pairs 8 consecutive ones.  With half-split
+// pairs lane l < R/8 holds [4l, 4l + 4) and [R/2 + 4l, R/2 + 4l + 4), so that both columns of a
+// pair are in one lane and no exchange between lanes is needed (two 8-byte accesses instead of
+// one of 16 bytes; exchanging the halves by shuffles measured 1,189 us where this takes 1,076);
+// the lanes behind hold the columns that do not turn, 8 consecutive ones each.
 struct NormRopeTensor {
   const void* in;
   void* out;
@@ -158,36 +239,40 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   const bool live = n < a.N && 8 * l < a.D;
   const int b = blockIdx.z;
   const bool turned = a.table != nullptr && 8 * l < a.rot;
-  const int half = a.rot / 16;                            // lanes of one half (kHalves)
+  // columns [c0, c0 + 4) and [c1, c1 + 4); pairs [c0 / 2, ...) or [4l, ...)
+  const int c0 = kHalves && turned ? 4 * l : 8 * l;
+  const int c1 = kHalves && turned ? a.rot / 2 + 4 * l : 8 * l + 4;
 
   // the row's (cos, sin) pairs this lane needs, read once and used for every head
-  float cs[kHalves ? 16 : 8];
+  float cs[8];
   if (live && turned) {
-    const int pair0 = kHalves ? 8 * (l < half ? l : l - half) : 4 * l;
-    const float4* src = reinterpret_cast<const float4*>(a.table + b * a.table_b +
-                                                        n * a.rot + 2 * pair0);
+    const float4* src =
+        reinterpret_cast<const float4*>(a.table + b * a.table_b + n * a.rot + 8 * l);
 #pragma unroll
-    for (int i = 0; i < (kHalves ? 4 : 2); ++i) {
+    for (int i = 0; i < 2; ++i) {
       const float4 v = src[i];
       cs[4 * i] = v.x; cs[4 * i + 1] = v.y; cs[4 * i + 2] = v.z; cs[4 * i + 3] = v.w;
     }
   }
-  // the other half of each pair lies rot/16 lanes away in the same row
-  const int partner = (lane - l) + (l < half ? l + half : (l < 2 * half ? l - half : l));
-  const float sign = l < half ? -1.f : 1.f;
 
   const int which = blockIdx.y / a.chunks;
   const NormRopeTensor& t = a.t[which];
   const int h0 = (blockIdx.y - which * a.chunks) * a.heads_per_cta;
   const int h1 = min(h0 + a.heads_per_cta, a.H);
-  const T* in = static_cast<const T*>(t.in) + b * t.in_b + n * t.in_n + 8 * l;
-  T* out = static_cast<T*>(t.out) + b * t.out_b + n * t.out_n + 8 * l;
-  const T* weight = static_cast<const T*>(t.weight) + 8 * l;
+  const T* in = static_cast<const T*>(t.in) + b * t.in_b + n * t.in_n;
+  T* out = static_cast<T*>(t.out) + b * t.out_b + n * t.out_n;
+  const T* weight = static_cast<const T*>(t.weight);
+  auto load8 = [&](Vec8<T>& v, const T* row) {
+    if (kHalves)
+      v.load(row + c0, row + c1);
+    else
+      v.load(row + c0);
+  };
   const bool weighted = a.norm && t.weight != nullptr && live;
   float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
   if (weighted) {
     Vec8<T> wv;
-    wv.load(weight);
+    load8(wv, weight);
     wv.unpack(w);
   }
 
@@ -195,7 +280,7 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
     Vec8<T> v[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (live && h + i < h1) v[i].load(in + (h + i) * t.in_h);
+      if (live && h + i < h1) load8(v[i], in + (h + i) * t.in_h);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       if (h + i >= h1) break;                             // the same for the whole warp
@@ -210,29 +295,30 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
         const float r = __frsqrt_rn(fmaf(ss, a.inv_d, a.eps));
         if (a.weight_h != 0 && weighted) {
           Vec8<T> wv;
-          wv.load(weight + (h + i) * a.weight_h);
+          load8(wv, weight + (h + i) * a.weight_h);
           wv.unpack(w);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] *= r * w[j];
       }
-      if (a.table != nullptr) {
-        if (kHalves) {
+      if (turned) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float y = __shfl_sync(0xffffffffu, x[j], partner);
-            if (turned) x[j] = fmaf(x[j], cs[2 * j], sign * y * cs[2 * j + 1]);
-          }
-        } else if (turned) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float u = x[2 * j], z = x[2 * j + 1], c = cs[2 * j], sn = cs[2 * j + 1];
-            x[2 * j] = fmaf(u, c, -z * sn);
-            x[2 * j + 1] = fmaf(u, sn, z * c);
-          }
+        for (int j = 0; j < 4; ++j) {
+          // pair j: columns j of both groups, or neighbours
+          float& p = x[kHalves ? j : 2 * j];
+          float& q = x[kHalves ? j + 4 : 2 * j + 1];
+          const float u = p, z = q, c = cs[2 * j], sn = cs[2 * j + 1];
+          p = fmaf(u, c, -z * sn);
+          q = fmaf(u, sn, z * c);
         }
       }
-      if (live) Vec8<T>::store(out + (h + i) * t.out_h, x);
+      if (live) {
+        T* row = out + (h + i) * t.out_h;
+        if (kHalves)
+          Vec8<T>::store(row + c0, row + c1, x);
+        else
+          Vec8<T>::store(row + c0, x);
+      }
     }
   }
 }
