@@ -222,6 +222,8 @@ LINEAR_CASES = [
     (1, 1000, 512, 1536, "bf16", 4, "bgr", None, None),
     (2, 700, 328, 520, "fp16", 0, "br", "silu", None),
     (1, 2100, 256, 2304, "bf16", 0, "b", None, 18),
+    (1, 9001, 72, 9000, "bf16", 0, "bgr", "gelu_tanh", None),
+    (2, 5300, 128, 4608, "fp16", 2, "r", None, 36),
     (1, 1, 1, 1, "fp32", 0, "bgr", "gelu", None),
     (2, 33, 67, 101, "fp32", 0, "bgr", "silu", None),
     (1, 192, 128, 512, "fp32", 2, "b", "gelu_tanh", None),
@@ -296,6 +298,9 @@ QKV_CASES = [
     (1, 700, 512, 7, 64, "fp16", 0, True, True, "shared", (16, 16), True),
     (1, 1030, 136, 6, 128, "bf16", 0, True, True, "shared", (44, 42, 42), False),
     (2, 515, 192, 9, 64, "bf16", 0, False, True, "head", (24, 20, 20), False),
+    (1, 2100, 128, 7, 128, "fp16", 0, True, True, "shared", (16, 56, 56), True),
+    (1, 8200, 64, 17, 128, "bf16", 0, True, True, "head", (44, 42, 42), False),
+    (2, 4700, 64, 33, 64, "bf16", 0, True, True, "shared", (16, 16), True),
 ]
 
 

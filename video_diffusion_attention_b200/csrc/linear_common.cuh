@@ -32,15 +32,31 @@ struct LinearArgs {
 };
 
 // Activations on the fp32 accumulator (numbering of tara_act).
-__device__ __forceinline__ float apply_act(float v, int act) {
-  if (act == 1) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-  if (act == 2) {
+template <int kAct>
+__device__ __forceinline__ float activate(float v) {
+  if (kAct == 1) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  if (kAct == 2) {
     // v/2 (1 + tanh u) = v / (1 + exp(-2u))
     const float u = 0.79788456080286536f * (v + 0.044715f * v * v * v);
     return __fdividef(v, 1.0f + __expf(-2.0f * u));
   }
-  if (act == 3) return __fdividef(v, 1.0f + __expf(-v));
+  if (kAct == 3) return __fdividef(v, 1.0f + __expf(-v));
   return v;
+}
+// In place on a thread's values; the branch on the activation is taken once.
+template <int kN>
+__device__ __forceinline__ void activate_all(float (&f)[kN], int act) {
+  if (act == 0) return;
+  if (act == 1) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) f[i] = activate<1>(f[i]);
+  } else if (act == 2) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) f[i] = activate<2>(f[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) f[i] = activate<3>(f[i]);
+  }
 }
 
 __device__ __forceinline__ float to_f32(float v) { return v; }

@@ -1,5 +1,5 @@
 // linear_ptx.cuh -- inline-PTX wrappers the linear-layer kernels need beyond sm100_ptx.cuh:
-// TMA loads of weight tiles (2-D) and token views (4-D), TMA stores, and short TMEM loads.
+// TMA loads of weight tiles (2-D) and token views (4-D), short TMEM loads, suspended waits.
 // No cluster multicast.
 #pragma once
 
@@ -28,26 +28,6 @@ __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// Tile store from shared memory; elements outside the tensor are not written.
-__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int x, int y,
-                                             int z, int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
-          reinterpret_cast<uint64_t>(map)),
-      "r"(x), "r"(y), "r"(z), "r"(w), "r"(src)
-      : "memory");
-}
-__device__ __forceinline__ void bulk_commit() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// Every committed store of this thread has read its shared memory / has completed.
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-__device__ __forceinline__ void bulk_wait_all() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-
 // 32 lanes x 8 consecutive 32-bit columns.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -67,12 +47,46 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 }
 
 constexpr uint64_t kLinWaitNs = 2000000000ull;    // 2 s per wait; a normal wait is microseconds
+constexpr uint32_t kLinIdleNs = 1000000u;           // 1 ms between looks at the clock
 constexpr uint64_t kLinDrainNs = 200000000ull;    // 0.2 s to let in-flight MMAs land
+
+// One try of up to `hint_ns`: the thread is suspended by the hardware, not polling, until the
+// phase completes or the hint runs out.
+__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity,
+                                                  uint32_t hint_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded wait as mbar_wait, suspended between looks at the clock: waits here last up to a
+// tile's products (tens of microseconds), and ten polling warps an SM cost issue slots and
+// power.
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity,
+                                               volatile int* abort) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait_for(a, parity, kLinIdleNs)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait_for(a, parity, kLinIdleNs)) {
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > kLinWaitNs) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
 
 // Bounded wait of a whole warp: true only when every lane saw the phase complete.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
                                                volatile int* abort) {
-  const bool ok = mbar_wait(bar, parity, abort, kLinWaitNs);
+  const bool ok = mbar_wait_idle(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -84,6 +98,21 @@ template <bool kBF16>
 __device__ __forceinline__ float2 unpack16(uint32_t w) {
   if (kBF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// 8 consecutive 16-bit values as fp32.
+template <bool kBF16>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = unpack16<kBF16>(w[i]);
+    f[2 * i] = t.x;
+    f[2 * i + 1] = t.y;
+  }
+}
+__device__ __forceinline__ uint4 ldg16(const void* base, long long i) {   // i: 16-bit elements
+  return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i));
 }
 
 }  // namespace tara

@@ -56,9 +56,10 @@ linear_simt_kernel(const __grid_constant__ LinearArgs a) {
     for (int j = 0; j < 4; ++j) {
       const int c = c0 + tc + j;
       if (c >= a.C) continue;
-      float v = acc[i][j];
-      if (a.bias) v += to_f32(static_cast<const T*>(a.bias)[c]);
-      v = apply_act(v, a.act);
+      float one[1] = {acc[i][j]};
+      if (a.bias) one[0] += to_f32(static_cast<const T*>(a.bias)[c]);
+      activate_all(one, a.act);
+      float v = one[0];
       if (a.gate) v *= to_f32(static_cast<const T*>(a.gate)[b * a.gate_b + c]);
       if (a.residual.ptr)
         v += to_f32(static_cast<const T*>(a.residual.ptr)[row_offset(a.residual, b, n, c)]);

@@ -15,6 +15,9 @@
 #include "linear_pair.cuh"
 #include "linear_simt.cuh"
 #include "norm_rope.cuh"
+#ifndef LIN_BIG
+#define LIN_BIG 1000000
+#endif
 
 namespace tara {
 namespace {
@@ -135,16 +138,16 @@ int encode_weights(const DeviceInfo& dev, CUtensorMap* map, tara_dtype dt, const
   return encode_map(dev, map, dt, w, 2, dims, strides, box_rows);
 }
 
-template <bool kBF16, int BN, bool kQkv>
+template <bool kBF16, int BN, int kSubs, bool kQkv>
 struct PairLauncher {
   static int allow(const DeviceInfo& dev) {
     static std::mutex mu;
     static uint64_t done = 0;   // one bit per device
     std::lock_guard<std::mutex> lock(mu);
     if (done >> dev.index & 1) return TARA_OK;
-    if (cudaFuncSetAttribute(linear_pair_kernel<kBF16, BN, kQkv>,
+    if (cudaFuncSetAttribute(linear_pair_kernel<kBF16, BN, kSubs, kQkv>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             PairLin<BN>::kSmemBytes) != cudaSuccess)
+                             PairLin<BN, kSubs>::kSmemBytes) != cudaSuccess)
       return TARA_ERR_CUDA;
     done |= (uint64_t)1 << dev.index;
     return TARA_OK;
@@ -159,18 +162,14 @@ struct PairLauncher {
     if ((rc = encode_view(dev, &maps.x, dt, a.x, a.B, a.N, a.K, 128)) != TARA_OK ||
         (rc = encode_weights(dev, &maps.w, dt, a.w, a.C, a.K, BN / 2)) != TARA_OK)
       return rc;
-    const int parts = a.C / a.part_cols;
-    for (int i = 0; i < 3; ++i) {
-      const RowView& y = a.y[i < parts ? i : 0];
-      if ((rc = encode_view(dev, &maps.y[i], dt, y, a.B, a.N, a.part_cols, 32)) != TARA_OK) return rc;
-    }
-    p.m_tiles = (int)(((long long)a.N + 255) / 256);
+    constexpr int rows = 256 * kSubs;
+    p.m_tiles = (int)(((long long)a.N + rows - 1) / rows);
     p.n_tiles = (int)(((long long)a.C + BN - 1) / BN);
-    p.group = 8;
+    p.group = 8 / kSubs;
     const long long tiles = (long long)a.B * p.m_tiles * p.n_tiles;
     const long long clusters = std::min<long long>(tiles, std::max(1, dev.sms / 2));
-    linear_pair_kernel<kBF16, BN, kQkv>
-        <<<(unsigned)(2 * clusters), kPairLinThreads, PairLin<BN>::kSmemBytes, stream>>>(maps, p);
+    linear_pair_kernel<kBF16, BN, kSubs, kQkv>
+        <<<(unsigned)(2 * clusters), kPairLinThreads, PairLin<BN, kSubs>::kSmemBytes, stream>>>(maps, p);
     return launched();
   }
 };
@@ -192,11 +191,11 @@ void merge_branches(LinearArgs* a) {
   a->B = 1;
 }
 
-template <bool kBF16, int BN>
+template <bool kBF16, int BN, int kSubs>
 int launch_pair(const DeviceInfo& dev, const PairLinArgs& p, bool heads, tara_dtype dt,
                 cudaStream_t stream) {
-  return heads ? PairLauncher<kBF16, BN, true>::launch(dev, p, dt, stream)
-               : PairLauncher<kBF16, BN, false>::launch(dev, p, dt, stream);
+  return heads ? PairLauncher<kBF16, BN, kSubs, true>::launch(dev, p, dt, stream)
+               : PairLauncher<kBF16, BN, kSubs, false>::launch(dev, p, dt, stream);
 }
 
 // head: the norm and rotation of a projection's q and k, or nullptr.
@@ -221,13 +220,19 @@ int run_linear(LinearArgs a, const HeadArgs* head, tara_dtype dt, cudaStream_t s
   PairLinArgs p{};
   p.lin = a;
   if (head) p.head = *head;
-  // 256 columns a tile halve the loads of x per product; 128 where 256 would leave SM pairs idle
-  const bool wide = tiles128 / 2 >= dev.sms / 2;
-  if (dt == TARA_BF16)
-    return wide ? launch_pair<true, 256>(dev, p, head != nullptr, dt, stream)
-                : launch_pair<true, 128>(dev, p, head != nullptr, dt, stream);
-  return wide ? launch_pair<false, 256>(dev, p, head != nullptr, dt, stream)
-              : launch_pair<false, 128>(dev, p, head != nullptr, dt, stream);
+  // 256 columns a tile halve the loads of x per product, two sub-tiles those of W; the smaller
+  // tiles where the larger would leave SM pairs idle
+  const int pairs = std::max(1, dev.sms / 2);
+  const int size = tiles128 / 4 >= LIN_BIG * pairs ? 2 : (tiles128 / 2 >= pairs ? 1 : 0);
+  const bool heads = head != nullptr;
+  if (dt == TARA_BF16) {
+    if (size == 2) return launch_pair<true, 256, 2>(dev, p, heads, dt, stream);
+    if (size == 1) return launch_pair<true, 256, 1>(dev, p, heads, dt, stream);
+    return launch_pair<true, 128, 1>(dev, p, heads, dt, stream);
+  }
+  if (size == 2) return launch_pair<false, 256, 2>(dev, p, heads, dt, stream);
+  if (size == 1) return launch_pair<false, 256, 1>(dev, p, heads, dt, stream);
+  return launch_pair<false, 128, 1>(dev, p, heads, dt, stream);
 }
 
 // The whole per-token column count of a view.
