@@ -223,6 +223,12 @@ LINEAR_CASES = [
     (2, 700, 328, 520, "fp16", 0, "br", "silu", None),
     (1, 2100, 256, 2304, "bf16", 0, "b", None, 18),
     (1, 9001, 72, 9000, "bf16", 0, "bgr", "gelu_tanh", None),
+    (1, 1, 4096, 1024, "bf16", 0, "bgr", "silu", 8),
+    (1, 16, 2056, 392, "fp16", 0, "br", None, None),
+    (5, 3, 1024, 256, "bf16", 8, "bgr", "gelu", 2),
+    (2, 31, 2048, 128, "bf16", 16, "bgr", None, None),
+    (1, 255, 1024, 640, "fp16", 0, "r", "gelu_tanh", None),
+    (1, 7, 64, 24000, "bf16", 0, "bg", None, None),
     (2, 5300, 128, 4608, "fp16", 2, "r", None, 36),
     (1, 1, 1, 1, "fp32", 0, "bgr", "gelu", None),
     (2, 33, 67, 101, "fp32", 0, "bgr", "silu", None),
@@ -298,6 +304,10 @@ QKV_CASES = [
     (1, 700, 512, 7, 64, "fp16", 0, True, True, "shared", (16, 16), True),
     (1, 1030, 136, 6, 128, "bf16", 0, True, True, "shared", (44, 42, 42), False),
     (2, 515, 192, 9, 64, "bf16", 0, False, True, "head", (24, 20, 20), False),
+    (3, 20, 1024, 3, 64, "bf16", 8, True, True, "head", (48,), True),
+    (1, 17, 1032, 4, 128, "fp16", 0, True, True, "shared", (40,), False),
+    (2, 120, 512, 2, 128, "bf16", 0, True, False, None, (96,), True),
+    (1, 16, 192, 40, 64, "bf16", 0, False, True, "shared", (16, 24, 24), False),
     (1, 2100, 128, 7, 128, "fp16", 0, True, True, "shared", (16, 56, 56), True),
     (1, 8200, 64, 17, 128, "bf16", 0, True, True, "head", (44, 42, 42), False),
     (2, 4700, 64, 33, 64, "bf16", 0, True, True, "shared", (16, 16), True),

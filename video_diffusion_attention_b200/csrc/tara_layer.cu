@@ -14,6 +14,7 @@
 #include "layer_checks.h"
 #include "linear_pair.cuh"
 #include "linear_simt.cuh"
+#include "linear_skinny.cuh"
 #include "norm_rope.cuh"
 #ifndef LIN_BIG
 #define LIN_BIG 1000000
@@ -198,6 +199,72 @@ int launch_pair(const DeviceInfo& dev, const PairLinArgs& p, bool heads, tara_dt
                : PairLauncher<kBF16, BN, kSubs, false>::launch(dev, p, dt, stream);
 }
 
+template <bool kBF16, int kT, bool kQkv>
+int launch_skinny(const DeviceInfo& dev, SkinnyArgs p, int zs, tara_dtype dt, cudaStream_t stream) {
+  using S = SkinnyLin<kT>;
+  static std::mutex mu;
+  static uint64_t done = 0;   // one bit per device
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!(done >> dev.index & 1)) {
+      if (cudaFuncSetAttribute(linear_skinny_kernel<kBF16, kT, kQkv>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               S::kSmemBytes) != cudaSuccess)
+        return TARA_ERR_CUDA;
+      done |= (uint64_t)1 << dev.index;
+    }
+  }
+  const LinearArgs& a = p.lin;
+  PairLinMaps maps;
+  RowView x = a.x;
+  if (p.rows != a.N && a.N == 1) x.n = x.b;            // the branches run on as rows
+  int rc;
+  if ((rc = encode_view(dev, &maps.x, dt, x, zs, p.rows, a.K, kT)) != TARA_OK ||
+      (rc = encode_weights(dev, &maps.w, dt, a.w, a.C, a.K, 128)) != TARA_OK)
+    return rc;
+  const long long c_tiles = ((long long)a.C + 127) / 128, t_tiles = ((long long)p.rows + kT - 1) / kT;
+  // K is split so that the CTAs fill whole rounds of the 2 an SM that run together; a CTA's
+  // start and end cost about as much as 8 of its K steps
+  const long long tiles = c_tiles * t_tiles * zs, slots = 2LL * dev.sms, steps = (a.K + 63) / 64;
+  long long best = 0;
+  for (int s = 1; s <= 8 && s <= steps; s *= 2) {
+    const long long cost = (tiles * s + slots - 1) / slots * ((steps + s - 1) / s + 8);
+    if (s == 1 || cost < best) {
+      best = cost;
+      p.splits = s;
+    }
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(c_tiles * p.splits), (unsigned)t_tiles, (unsigned)zs);
+  cfg.blockDim = dim3(kSkinnyThreads);
+  cfg.dynamicSmemBytes = S::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)p.splits;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, linear_skinny_kernel<kBF16, kT, kQkv>, maps, p) == cudaSuccess
+             ? TARA_OK
+             : TARA_ERR_CUDA;
+}
+
+template <bool kBF16, bool kQkv>
+int launch_skinny_rows(const DeviceInfo& dev, const SkinnyArgs& p, int zs, tara_dtype dt,
+                       cudaStream_t stream) {
+  if (p.rows <= 16) return launch_skinny<kBF16, 16, kQkv>(dev, p, zs, dt, stream);
+  if (p.rows <= 32) return launch_skinny<kBF16, 32, kQkv>(dev, p, zs, dt, stream);
+  if (p.rows <= 64) return launch_skinny<kBF16, 64, kQkv>(dev, p, zs, dt, stream);
+  return launch_skinny<kBF16, 128, kQkv>(dev, p, zs, dt, stream);
+}
+
+// Rows up to which the weight-streaming kernel is taken.
+#ifndef SKINNY_ROWS
+#define SKINNY_ROWS 256
+#endif
+constexpr long long kSkinnyRows = SKINNY_ROWS;
+
 // head: the norm and rotation of a projection's q and k, or nullptr.
 int run_linear(LinearArgs a, const HeadArgs* head, tara_dtype dt, cudaStream_t stream) {
   if (dt == TARA_FP32) {
@@ -212,6 +279,21 @@ int run_linear(LinearArgs a, const HeadArgs* head, tara_dtype dt, cudaStream_t s
   int rc = device_info(&dev);
   if (rc != TARA_OK) return rc;
   a.status = dev.status;
+  const bool heads = head != nullptr;
+  if ((long long)a.B * a.N <= kSkinnyRows) {
+    SkinnyArgs p{};
+    p.lin = a;
+    if (head) p.head = *head;
+    // one run of rows over all branches where x allows it: W is read once
+    const bool runs_on = a.B == 1 || a.N == 1 || a.x.b == a.x.n * a.N;
+    p.rows = runs_on ? a.B * a.N : a.N;
+    const int zs = runs_on ? 1 : a.B;
+    if (dt == TARA_BF16)
+      return heads ? launch_skinny_rows<true, true>(dev, p, zs, dt, stream)
+                   : launch_skinny_rows<true, false>(dev, p, zs, dt, stream);
+    return heads ? launch_skinny_rows<false, true>(dev, p, zs, dt, stream)
+                 : launch_skinny_rows<false, false>(dev, p, zs, dt, stream);
+  }
   if (!head || !head->table) merge_branches(&a);
   // the kernel numbers its tiles in int
   const long long tiles128 = (long long)a.B * (((long long)a.N + 255) / 256) *
@@ -224,7 +306,6 @@ int run_linear(LinearArgs a, const HeadArgs* head, tara_dtype dt, cudaStream_t s
   // tiles where the larger would leave SM pairs idle
   const int pairs = std::max(1, dev.sms / 2);
   const int size = tiles128 / 4 >= LIN_BIG * pairs ? 2 : (tiles128 / 2 >= pairs ? 1 : 0);
-  const bool heads = head != nullptr;
   if (dt == TARA_BF16) {
     if (size == 2) return launch_pair<true, 256, 2>(dev, p, heads, dt, stream);
     if (size == 1) return launch_pair<true, 256, 1>(dev, p, heads, dt, stream);
