@@ -23,12 +23,24 @@
 // weights are the same for all lanes and come through L1.
 #pragma once
 
+#include <type_traits>
+
 #include "linear_common.cuh"
 #include "linear_ptx.cuh"
 
 namespace tara {
 
-constexpr int kPairLinThreads = 320;   // warp 0 loads, warp 1 issues MMAs, warps 2-9 epilogue
+// Warp 0 loads, warp 1 issues MMAs, warps 4-11 are the epilogue (warps 2 and 3 complete the
+// control warpgroup).  The launch gives every thread kPairLinRegs registers; the control
+// warpgroup lowers its share and the two epilogue warpgroups raise theirs.  The sum must equal
+// the launch pool, or the raise would wait for registers that never come; the host refuses to
+// launch when ptxas gave the kernel another count.
+constexpr int kPairLinThreads = 384;
+constexpr int kPairLinRegs = 168;
+constexpr int kPairLinControlRegs = 88;
+constexpr int kPairLinEpilogueRegs = 208;
+static_assert(128 * kPairLinControlRegs + 256 * kPairLinEpilogueRegs == kPairLinThreads * kPairLinRegs,
+              "register split must use the launch pool exactly");
 
 template <int BN, int kSubs>
 struct PairLin {
@@ -78,144 +90,247 @@ __device__ __forceinline__ uint32_t stage128(uint32_t buf, int row, int chunk) {
 struct PairWarp {
   uint32_t acc;      // tensor memory: lane quarter and first column
   uint32_t buf;      // staging
+  uint32_t release;  // shared::cluster address of the accumulator's acc_empty barrier
   int b, r0, c0, lane;
 };
 
-// 32 columns of the residual: 4 lanes a row, 8 rows a load.
-__device__ __forceinline__ void pair_load_residual(const LinearArgs& a, const PairWarp& w, int cc,
-                                                   uint4 (&res)[4]) {
-  const int c = cc + (w.lane & 3) * 8;
-  const int row = w.r0 + (w.lane >> 2);
-  const bool c_ok = c < a.C;
-  const uint16_t* p = static_cast<const uint16_t*>(a.residual.ptr) +
-                      row_offset(a.residual, w.b, row, c_ok ? c : 0);
+// The warp has read its part of the accumulator: the MMA warp may start the unit after next in it.
+__device__ __forceinline__ void pair_release(const PairWarp& w) {
+  tc_fence_before();
+  __syncwarp();
+  if (w.lane == 0) mbar_arrive_cluster(w.release);
+}
+
+// Two things make this epilogue cheap or dear.  Instruction fetch: its code runs once a tile
+// between long waits, so unrolled straight-line code costs about 10 cycles an instruction and a
+// skipped branch as much as a taken one; the loops below are kept rolled and their bodies small
+// (fully unrolled, a unit of 128 columns took 6,600 cycles).  And its arguments: behind the
+// barriers and shared-memory accesses, which are opaque to the compiler, they would be fetched
+// again each time, so what the loops read is gathered in registers before the products are
+// complete.
+struct PairLinearAhead {
+  uint16_t* y[2];            // this lane's chunk of each 64 columns' first piece, first row
+  const uint16_t* r[2];      // the same of the residual
+  long long y_n[2], r_n;     // row strides
+  const uint16_t *bias, *gate;
+  int cols, rows;            // columns and rows of the warp's part that exist
+  bool with_res;
+  uint4 res[4];              // the next piece of the residual
+};
+
+// 32 columns of the residual from this lane's chunk at `src`: 4 lanes a row, 8 rows a load.
+__device__ __forceinline__ void pair_load_residual(const PairLinearAhead& ah, int lane,
+                                                   const uint16_t* src, int cols, uint4 (&res)[4]) {
+  const int row = lane >> 2;
+  const bool c_ok = (lane & 3) * 8 < cols;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     res[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (c_ok && row + i * 8 < a.N)
-      res[i] = *reinterpret_cast<const uint4*>(p + (long long)(i * 8) * a.residual.n);
+    if (c_ok && row + i * 8 < ah.rows)
+      res[i] = *reinterpret_cast<const uint4*>(src + (long long)(i * 8) * ah.r_n);
   }
 }
 
-// The staged piece -> y: blocks of eight columns from column `col` (of the output's row) of this
-// lane's chunk; `ok`: the chunk is inside the output.
-__device__ __forceinline__ void pair_store(const LinearArgs& a, const RowView& y, const PairWarp& w,
-                                           int col, bool ok) {
-  const int row = w.lane >> 2;
-  uint16_t* p = static_cast<uint16_t*>(const_cast<void*>(y.ptr)) +
-                row_offset(y, w.b, w.r0 + row, col);
+__device__ __forceinline__ void pair_linear_ahead(const LinearArgs& a, const PairWarp& w,
+                                                  PairLinearAhead& ah) {
+  ah.cols = min(128, a.C - w.c0);
+  ah.rows = min(32, a.N - w.r0);
+  ah.bias = a.bias ? static_cast<const uint16_t*>(a.bias) + w.c0 : nullptr;
+  ah.gate = a.gate ? static_cast<const uint16_t*>(a.gate) + w.b * a.gate_b + w.c0 : nullptr;
+  ah.with_res = a.residual.ptr != nullptr;
+  ah.r_n = a.residual.n;
+  const int row = w.r0 + (w.lane >> 2);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 v = ld_shared_v4(stage64(w.buf, row + i * 8, w.lane & 3));
-    if (ok && w.r0 + row + i * 8 < a.N)
-      *reinterpret_cast<uint4*>(p + (long long)(i * 8) * y.n) = v;
+  for (int p = 0; p < 2; ++p) {
+    // heads and parts begin at multiples of 64 columns (or there is one of each)
+    const int c = min(w.c0 + p * 64, a.C - 8);
+    const int part = c < a.part_cols ? 0 : c / a.part_cols;
+    const RowView& y = a.y[part];
+    ah.y[p] = static_cast<uint16_t*>(const_cast<void*>(y.ptr)) +
+              row_offset(y, w.b, row, c - part * a.part_cols) + (w.lane & 3) * 8;
+    ah.y_n[p] = y.n;
+    ah.r[p] = nullptr;
+    if (ah.with_res)
+      ah.r[p] = static_cast<const uint16_t*>(a.residual.ptr) + row_offset(a.residual, w.b, row, c) +
+                (w.lane & 3) * 8;
   }
+  if (ah.with_res) pair_load_residual(ah, w.lane, ah.r[0], ah.cols, ah.res);
 }
 
-// residual + gate * act(accumulator + bias) of the warp's 128 columns.  `res`: the first piece
-// of the residual.
-template <bool kBF16>
-__device__ __forceinline__ void pair_linear(const LinearArgs& a, const PairWarp& w, uint4 (&res)[4]) {
-  const bool with_res = a.residual.ptr != nullptr;
+// residual + gate * act(accumulator + bias) of the warp's 128 columns, 32 at a time.
+template <bool kBF16, int kAct>
+__device__ __forceinline__ void pair_linear(const PairWarp& w, PairLinearAhead& ah) {
 #pragma unroll 1
-  for (int p = 0; p < 128; p += 32) {
-    const int cc = w.c0 + p;
-    if (cc >= a.C) break;
+  for (int p = 0; p < 4; ++p) {
+    const int left = ah.cols - p * 32;
+    if (left <= 0) break;
     uint32_t v[32];
-    tmem_ld32(w.acc + p, v);
-    uint4 bias[4], gate[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int c = cc + q * 8;
-      bias[q] = gate[q] = make_uint4(0u, 0u, 0u, 0u);
-      if (a.bias && c < a.C) bias[q] = ldg16(a.bias, c);
-      if (a.gate && c < a.C) gate[q] = ldg16(a.gate, w.b * a.gate_b + c);
-    }
-    if (with_res) {
+    tmem_ld32(w.acc + p * 32, v);
+    if (ah.with_res) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        st_shared_v4(stage64(w.buf, i * 8 + (w.lane >> 2), w.lane & 3), res[i].x, res[i].y, res[i].z,
-                     res[i].w);
+        st_shared_v4(stage64(w.buf, i * 8 + (w.lane >> 2), w.lane & 3), ah.res[i].x, ah.res[i].y,
+                     ah.res[i].z, ah.res[i].w);
       __syncwarp();
-      if (p < 96) pair_load_residual(a, w, cc + 32, res);
+      if (left > 32)
+        pair_load_residual(ah, w.lane, (p >= 1 ? ah.r[1] : ah.r[0]) + (p == 1 ? 0 : 32), left - 32,
+                           ah.res);
     }
     tmem_ld_wait();
     reg_fence<32>(v);
+    float f[32];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t slot = stage64(w.buf, w.lane, q);
-      float f[8];
+    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+    // blocks of eight columns behind the last one keep what they have; they are not stored
+    if (ah.bias) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[q * 8 + i]);
-      if (a.bias) {
+      for (int q = 0; q < 4; ++q) {
         float t[8];
-        unpack8<kBF16>(bias[q], t);
+        unpack8<kBF16>(ldg16(ah.bias, min(p * 32 + q * 8, ah.cols - 8)), t);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] += t[i];
+        for (int i = 0; i < 8; ++i) f[q * 8 + i] += t[i];
       }
-      activate_all(f, a.act);
-      if (a.gate) {
-        float t[8];
-        unpack8<kBF16>(gate[q], t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= t[i];
-      }
-      if (with_res) {
-        float t[8];
-        unpack8<kBF16>(ld_shared_v4(slot), t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] += t[i];
-      }
-      st_shared_v4(slot, pack16<kBF16>(f[0], f[1]), pack16<kBF16>(f[2], f[3]),
-                   pack16<kBF16>(f[4], f[5]), pack16<kBF16>(f[6], f[7]));
     }
-    __syncwarp();
-    const int part = cc / a.part_cols;     // parts begin at multiples of 64 columns
-    const int chunk_col = cc + (w.lane & 3) * 8;
-    pair_store(a, a.y[part], w, chunk_col < a.C ? chunk_col - part * a.part_cols : 0,
-               chunk_col < a.C);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = activate<kAct>(f[i]);
+    if (ah.gate) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float t[8];
+        unpack8<kBF16>(ldg16(ah.gate, min(p * 32 + q * 8, ah.cols - 8)), t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[q * 8 + i] *= t[i];
+      }
+    }
+    if (ah.with_res) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float t[8];
+        unpack8<kBF16>(ld_shared_v4(stage64(w.buf, w.lane, q)), t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[q * 8 + i] += t[i];
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      st_shared_v4(stage64(w.buf, w.lane, q), pack16<kBF16>(f[q * 8], f[q * 8 + 1]),
+                   pack16<kBF16>(f[q * 8 + 2], f[q * 8 + 3]),
+                   pack16<kBF16>(f[q * 8 + 4], f[q * 8 + 5]),
+                   pack16<kBF16>(f[q * 8 + 6], f[q * 8 + 7]));
+    if (p == 3 || left <= 32) pair_release(w);       // the last columns are in registers
+    else __syncwarp();
+    uint16_t* dst = ((p & 2) ? ah.y[1] : ah.y[0]) + (p & 1) * 32;
+    const long long stride = (p & 2) ? ah.y_n[1] : ah.y_n[0];
+    const int row = w.lane >> 2;
+    const bool ok = (w.lane & 3) * 8 < left;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 o = ld_shared_v4(stage64(w.buf, row + i * 8, w.lane & 3));
+      if (ok && row + i * 8 < ah.rows)
+        *reinterpret_cast<uint4*>(dst + (long long)(i * 8) * stride) = o;
+    }
     __syncwarp();
   }
 }
 
-// Bias of 8 columns from column c (zeros without one).
-template <bool kBF16>
-__device__ __forceinline__ void pair_bias8(const LinearArgs& a, int c, float (&f)[8]) {
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (a.bias) v = ldg16(a.bias, c);
-  unpack8<kBF16>(v, f);
-}
+// The same for the projection's epilogue.
+struct PairHeadsAhead {
+  const uint16_t *q_weight, *k_weight;   // nullptr: 1
+  const uint16_t* bias;      // at the warp's first column
+  const float* table;        // this lane's 16 bytes of the warp's first row (nullptr: no rotation)
+  long long weight_h;
+  int cols, rows, D, rot, halves, norm;
+  float eps, inv_d;
+  uint4 cs[8];               // the next piece of the table
+};
 
 // 16 (cos, sin) pairs, number 16 * piece on, of the warp's rows: 8 lanes a row, 4 rows a load.
-__device__ __forceinline__ void pair_load_table(const LinearArgs& a, const HeadArgs& head,
-                                                const PairWarp& w, int piece, uint4 (&cs)[8]) {
-  const int f = piece * 32 + (w.lane & 7) * 4;
-  const int row = w.r0 + (w.lane >> 3);
-  const float* p = head.table + w.b * head.table_b + (long long)row * head.rot + f;
+__device__ __forceinline__ void pair_load_table(const PairHeadsAhead& ah, int lane, int piece,
+                                                uint4 (&cs)[8]) {
+  const bool f_ok = piece * 32 + (lane & 7) * 4 < ah.rot;
+  const float* p = ah.table + piece * 32;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     cs[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (f < head.rot && row + i * 4 < a.N)
-      cs[i] = __ldg(reinterpret_cast<const uint4*>(p + (long long)(i * 4) * head.rot));
+    if (f_ok && (lane >> 3) + i * 4 < ah.rows)
+      cs[i] = __ldg(reinterpret_cast<const uint4*>(p + i * 4 * ah.rot));
   }
 }
 
-// Bias, norm and rotation of the heads in the warp's 128 columns.  `cs`: the first piece of the
-// table.
+__device__ __forceinline__ void pair_heads_ahead(const LinearArgs& a, const HeadArgs& head,
+                                                 const PairWarp& w, PairHeadsAhead& ah) {
+  ah.q_weight = static_cast<const uint16_t*>(head.weight[0]);
+  ah.k_weight = static_cast<const uint16_t*>(head.weight[1]);
+  ah.weight_h = head.weight_h;
+  ah.bias = a.bias ? static_cast<const uint16_t*>(a.bias) + w.c0 : nullptr;
+  ah.cols = min(128, a.C - w.c0);
+  ah.rows = min(32, a.N - w.r0);
+  ah.D = head.D;
+  ah.rot = head.rot;
+  ah.halves = head.halves;
+  ah.norm = head.norm;
+  ah.eps = head.eps;
+  ah.inv_d = head.inv_d;
+  ah.table = nullptr;
+  if (head.table) {
+    ah.table = head.table + w.b * head.table_b +
+               (long long)(w.r0 + (w.lane >> 3)) * head.rot + (w.lane & 7) * 4;
+    pair_load_table(ah, w.lane, 0, ah.cs);
+  }
+}
+
+// 8 accumulators from column d of a head: bias, norm (r: its factor) and weight.
 template <bool kBF16>
-__device__ __forceinline__ void pair_heads(const LinearArgs& a, const HeadArgs& head,
-                                           const PairWarp& w, uint4 (&cs)[8]) {
-  const int D = head.D;
-  const int half = head.rot / 2;
+__device__ __forceinline__ void pair_finish8(const uint32_t* v, const uint16_t* bias,
+                                             const uint16_t* weight, int d, float r, float* f) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(v[j]);
+  if (bias) {
+    float t[8];
+    unpack8<kBF16>(ldg16(bias, d), t);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] += t[j];
+  }
+  if (weight) {
+    float t[8];
+    unpack8<kBF16>(ldg16(weight, d), t);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= r * t[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= r;
+  }
+}
+
+template <bool kBF16>
+__device__ __forceinline__ void pair_stage8(uint32_t addr, const float* f) {
+  st_shared_v4(addr, pack16<kBF16>(f[0], f[1]), pack16<kBF16>(f[2], f[3]),
+               pack16<kBF16>(f[4], f[5]), pack16<kBF16>(f[6], f[7]));
+}
+
+// Bias, norm and rotation of the heads in the warp's 128 columns.
+template <bool kBF16>
+__device__ __forceinline__ void pair_heads(const LinearArgs& a, const PairWarp& w,
+                                           PairHeadsAhead& ah) {
+  const int D = ah.D;
+  const int half = ah.rot / 2;
 #pragma unroll 1
   for (int hd = 0; hd < 128; hd += D) {
+    if (hd >= ah.cols) break;
     const int c_h = w.c0 + hd;                         // the head's first column
-    if (c_h >= a.C) break;
-    const int part = c_h / a.part_cols;
+    const int part = c_h < a.part_cols ? 0 : c_h / a.part_cols;
     const int pc_h = c_h - part * a.part_cols;
-    const bool turn = part < 2 && head.table != nullptr;
-    const bool normed = part < 2 && head.norm;
+    const bool turn = part < 2 && ah.table != nullptr;
+    const bool normed = part < 2 && ah.norm;
+    const uint16_t* bias = ah.bias ? ah.bias + hd : nullptr;
+    const int h = part < 2 && ah.weight_h ? pc_h / D : 0;
+    const uint16_t* weight = !normed ? nullptr : (part == 0 ? ah.q_weight : ah.k_weight);
+    if (weight) weight += h * ah.weight_h;
     const uint32_t acc = w.acc + hd;
+    const RowView& y = a.y[part];                      // a head's columns lie in one row of y
+    uint16_t* out = static_cast<uint16_t*>(const_cast<void*>(y.ptr)) +
+                    row_offset(y, w.b, w.r0 + (w.lane >> 2), pc_h);
+    const long long out_n = y.n;
 
     float r = 1.f;
     if (normed) {
@@ -224,121 +339,143 @@ __device__ __forceinline__ void pair_heads(const LinearArgs& a, const HeadArgs& 
       for (int d = 0; d < D; d += 32) {
         uint32_t v[32];
         tmem_ld32(acc + d, v);
-        float t[4][8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) pair_bias8<kBF16>(a, c_h + d + q * 8, t[q]);
         tmem_ld_wait();
         reg_fence<32>(v);
+        if (bias) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float t[8];
+            unpack8<kBF16>(ldg16(bias, d + q * 8), t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              v[q * 8 + i] = __float_as_uint(__uint_as_float(v[q * 8 + i]) + t[i]);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float x = __uint_as_float(v[i]) + t[i >> 3][i & 7];
+          const float x = __uint_as_float(v[i]);
           ss[i & 3] = fmaf(x, x, ss[i & 3]);
         }
       }
-      r = __frsqrt_rn(fmaf((ss[0] + ss[1]) + (ss[2] + ss[3]), head.inv_d, head.eps));
+      r = __frsqrt_rn(fmaf((ss[0] + ss[1]) + (ss[2] + ss[3]), ah.inv_d, ah.eps));
     }
-    const void* weight = normed ? head.weight[part] : nullptr;
-    const long long w_h = pc_h / D * head.weight_h;
 
-    // Pieces.  Half-split pairs: blocks [j, j + 8), [j + 8, j + 16) of the low columns and their
-    // partners in the high ones, both halves of 16 pairs (then the columns behind R, 32 a piece);
-    // otherwise 32 neighbouring columns.  Piece i turns by the pairs from 16 i.
-    const bool split = turn && head.halves;
-    const int turning = turn ? (head.rot + 31) / 32 : 0;
-    const int pieces = split ? turning + (D - head.rot + 31) / 32 : D / 32;
+    // Pieces of four blocks of eight columns.  Half-split pairs: two low blocks and their
+    // partners in the high half, 16 pairs (then the columns behind R, 32 a piece); otherwise 32
+    // neighbouring columns.  Piece i turns by the pairs from 16 i, which lie in the staging
+    // buffer, 128 bytes a row; a thread overwrites the part of its own row that it has read with
+    // its output, block b at chunk 2b (pairs: low blocks at 0 and 4, high ones at 2 and 6).
+    const bool split = turn && ah.halves;
+    const int turning = turn ? (ah.rot + 31) / 32 : 0;
+    const int pieces = split ? turning + (D - ah.rot + 31) / 32 : D / 32;
 #pragma unroll 1
     for (int i = 0; i < pieces; ++i) {
       const bool pairs = split && i < turning;
-      const int first = pairs ? 16 * i : (split ? head.rot + 32 * (i - turning) : 32 * i);
-      const int limit = pairs ? half : D;              // blocks from here on do not exist
-      // first column of block q within the head
-      auto block = [&](int q) {
-        return pairs ? first + (q & 1) * 8 + (q >> 1) * half : first + q * 8;
-      };
-      auto exists = [&](int q) { return (pairs ? first + (q & 1) * 8 : first + q * 8) < limit; };
-      uint32_t v[32];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld8(acc + (exists(q) ? block(q) : 0), v + q * 8);
-      float t[32];
       const bool turned = turn && i < turning;
+      const int first = pairs ? 16 * i : (split ? ah.rot + 32 * (i - turning) : 32 * i);
+      const int last = pairs ? half : D;               // blocks from here on do not exist
       if (turned) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          st_shared_v4(stage128(w.buf, j * 4 + (w.lane >> 3), w.lane & 7), cs[j].x, cs[j].y, cs[j].z,
-                       cs[j].w);
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 c4 = ld_shared_v4(stage128(w.buf, w.lane, j));
-          t[4 * j] = __uint_as_float(c4.x);
-          t[4 * j + 1] = __uint_as_float(c4.y);
-          t[4 * j + 2] = __uint_as_float(c4.z);
-          t[4 * j + 3] = __uint_as_float(c4.w);
-        }
+          st_shared_v4(stage128(w.buf, j * 4 + (w.lane >> 3), w.lane & 7), ah.cs[j].x, ah.cs[j].y,
+                       ah.cs[j].z, ah.cs[j].w);
         __syncwarp();
         // the next piece's pairs: this head's, or the next head's first
-        pair_load_table(a, head, w, i + 1 < turning ? i + 1 : 0, cs);
-      }
-      float f[4][8];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int d = exists(q) ? block(q) : 0;
-        pair_bias8<kBF16>(a, c_h + d, f[q]);
-        if (q == 0) {
-          tmem_ld_wait();
-          reg_fence<32>(v);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[q][j] += __uint_as_float(v[q * 8 + j]);
-        if (normed) {
-          float g[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-          if (weight) unpack8<kBF16>(ldg16(weight, w_h + d), g);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[q][j] *= r * g[j];
-        }
+        pair_load_table(ah, w.lane, i + 1 < turning ? i + 1 : 0, ah.cs);
       }
       if (pairs) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float c = t[16 * q + 2 * j], s = t[16 * q + 2 * j + 1];
-            const float x = f[q][j], y = f[q + 2][j];
-            f[q][j] = fmaf(x, c, -y * s);
-            f[q + 2][j] = fmaf(x, s, y * c);
-          }
-      } else if (turned) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (first + q * 8 >= head.rot) break;
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          const int d = first + q * 8;
+          if (d >= last) break;
+          uint32_t v[16];
+          tmem_ld8(acc + d, v);
+          tmem_ld8(acc + d + half, v + 8);
+          float t[16];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float c = t[8 * q + 2 * j], s = t[8 * q + 2 * j + 1];
-            const float x = f[q][2 * j], y = f[q][2 * j + 1];
-            f[q][2 * j] = fmaf(x, c, -y * s);
-            f[q][2 * j + 1] = fmaf(x, s, y * c);
+            const uint4 c4 = ld_shared_v4(stage128(w.buf, w.lane, 4 * q + j));
+            t[4 * j] = __uint_as_float(c4.x);
+            t[4 * j + 1] = __uint_as_float(c4.y);
+            t[4 * j + 2] = __uint_as_float(c4.z);
+            t[4 * j + 3] = __uint_as_float(c4.w);
           }
+          tmem_ld_wait();
+          reg_fence<16>(v);
+          float f[16];
+          pair_finish8<kBF16>(v, bias, weight, d, r, f);
+          pair_finish8<kBF16>(v + 8, bias, weight, d + half, r, f + 8);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float x = f[j], z = f[j + 8], c = t[2 * j], s = t[2 * j + 1];
+            f[j] = fmaf(x, c, -z * s);
+            f[j + 8] = fmaf(x, s, z * c);
+          }
+          pair_stage8<kBF16>(stage128(w.buf, w.lane, 4 * q), f);
+          pair_stage8<kBF16>(stage128(w.buf, w.lane, 4 * q + 2), f + 8);
+        }
+      } else {
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          const int d = first + q * 8;
+          if (d >= last) break;
+          uint32_t v[8];
+          tmem_ld8(acc + d, v);
+          float t[8];
+          const bool turns = turned && d < ah.rot;
+          if (turns) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint4 c4 = ld_shared_v4(stage128(w.buf, w.lane, 2 * q + j));
+              t[4 * j] = __uint_as_float(c4.x);
+              t[4 * j + 1] = __uint_as_float(c4.y);
+              t[4 * j + 2] = __uint_as_float(c4.z);
+              t[4 * j + 3] = __uint_as_float(c4.w);
+            }
+          }
+          tmem_ld_wait();
+          reg_fence<8>(v);
+          float f[8];
+          pair_finish8<kBF16>(v, bias, weight, d, r, f);
+          if (turns) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float x = f[2 * j], z = f[2 * j + 1], c = t[2 * j], s = t[2 * j + 1];
+              f[2 * j] = fmaf(x, c, -z * s);
+              f[2 * j + 1] = fmaf(x, s, z * c);
+            }
+          }
+          pair_stage8<kBF16>(stage128(w.buf, w.lane, 2 * q), f);
         }
       }
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        st_shared_v4(stage64(w.buf, w.lane, q), pack16<kBF16>(f[q][0], f[q][1]),
-                     pack16<kBF16>(f[q][2], f[q][3]), pack16<kBF16>(f[q][4], f[q][5]),
-                     pack16<kBF16>(f[q][6], f[q][7]));
       __syncwarp();
+      // 4 lanes a row, one block each
       const int q = w.lane & 3;
-      pair_store(a, a.y[part], w, pc_h + (exists(q) ? block(q) : 0), exists(q));
+      const int d = pairs ? first + (q & 1) * 8 + (q >> 1) * half : first + q * 8;
+      const bool ok = (pairs ? first + (q & 1) * 8 : d) < last;
+      const int chunk = pairs ? (q & 1) * 4 + (q >> 1) * 2 : 2 * q;
+      const int row = w.lane >> 2;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 o = ld_shared_v4(stage128(w.buf, row + j * 8, chunk));
+        if (ok && row + j * 8 < ah.rows)
+          *reinterpret_cast<uint4*>(out + d + (long long)(j * 8) * out_n) = o;
+      }
       __syncwarp();
     }
   }
 }
 
-template <bool kBF16, int BN, int kSubs, bool kQkv>
+// kEpi: an activation (numbering of tara_act), or kEpiHeads for the projection.
+constexpr int kEpiHeads = 4;
+
+template <bool kBF16, int BN, int kSubs, int kEpi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairLinThreads, 1)
 linear_pair_kernel(const __grid_constant__ PairLinMaps maps,
                    const __grid_constant__ PairLinArgs args) {
   using S = PairLin<BN, kSubs>;
   constexpr int NS = S::kStages;
+  constexpr bool kQkv = kEpi == kEpiHeads;
   const LinearArgs& a = args.lin;
 
   extern __shared__ uint8_t smem_raw[];
@@ -411,8 +548,9 @@ linear_pair_kernel(const __grid_constant__ PairLinMaps maps,
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kPairLinControlRegs) : "memory");
+    if (warp == 0 && lane == 0) {
       // ------------------------------ TMA producer (both CTAs) -------------------------
       tma_prefetch_desc(&maps.x);
       tma_prefetch_desc(&maps.w);
@@ -455,9 +593,7 @@ linear_pair_kernel(const __grid_constant__ PairLinMaps maps,
         // even CTA, so give them 1 ms before this CTA's shared memory can be released
         for (int w = 0; w < 1000; ++w) __nanosleep(1000);
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    } else if (warp == 1 && lane == 0 && leader) {
       // ------------------------------ MMA issuer (even CTA) ----------------------------
       constexpr uint32_t idesc = make_idesc_f16(256, BN, kBF16, false);
       const uint64_t ad0 = make_sdesc_sw128(smem_u32(smem), 16, 1024);
@@ -530,13 +666,15 @@ linear_pair_kernel(const __grid_constant__ PairLinMaps maps,
       mbar_wait(drain, 0, &no_abort, kLinDrainNs);
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kPairLinEpilogueRegs) : "memory");
     // ------------------------------ epilogue warps (both CTAs) -------------------------
     const int wq = warp & 3;                 // TMEM lane quarter
-    const int grp = (warp - 2) >> 2;         // warpgroup: column half (256) or tile parity (128)
-    const int ew = warp - 2;
+    const int grp = (warp - 4) >> 2;         // warpgroup: column half (256) or tile parity (128)
+    const int ew = warp - 4;
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
     PairWarp w;
     w.buf = smem_u32(s_out + ew * 4096);
+    const uint32_t acc_empty_l = mapa_shared(smem_u32(acc_empty), 0);
     w.lane = lane;
     bool ok = true;
     uint32_t unit = 0;
@@ -551,27 +689,25 @@ linear_pair_kernel(const __grid_constant__ PairLinMaps maps,
         w.r0 = m0 + u * 256 + (int)rank * 128 + wq * 32;
         w.acc = tmem + lane_base + half * BN + (BN == 256 ? grp * 128 : 0);
         const bool live = w.r0 < a.N && w.c0 < a.C;
+        w.release = acc_empty_l + half * 8u;
         // the first piece of what comes from memory, in flight while the products run
-        uint4 ahead[kQkv ? 8 : 4];
+        typename std::conditional<kQkv, PairHeadsAhead, PairLinearAhead>::type ahead;
         if (live) {
-          if constexpr (kQkv) {
-            if (args.head.table) pair_load_table(a, args.head, w, 0, ahead);
-          } else {
-            if (a.residual.ptr) pair_load_residual(a, w, w.c0, ahead);
-          }
+          if constexpr (kQkv)
+            pair_heads_ahead(a, args.head, w, ahead);
+          else
+            pair_linear_ahead(a, w, ahead);
         }
         if (!(ok = mbar_wait_warp(&acc_full[half], (unit >> 1) & 1u, abort_flag))) break;
         tc_fence_after();
-        if (live) {
-          if constexpr (kQkv)
-            pair_heads<kBF16>(a, args.head, w, ahead);
-          else
-            pair_linear<kBF16>(a, w, ahead);
+        if constexpr (kQkv) {
+          if (live) pair_heads<kBF16>(a, w, ahead);
+          pair_release(w);
+        } else if (live) {
+          pair_linear<kBF16, kQkv ? 0 : kEpi>(w, ahead);   // releases the accumulator
+        } else {
+          pair_release(w);
         }
-        // the accumulator is read: the MMA warp may start the unit after next in it
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[half]), 0));
       }
     }
     tc_fence_before();

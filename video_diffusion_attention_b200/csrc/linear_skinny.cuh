@@ -23,11 +23,12 @@ struct SkinnyLin {
   static constexpr int kWBytes = 128 * 128;
   static constexpr int kXBytes = kT * 128;
   static constexpr int kStageBytes = kWBytes + kXBytes;
-  static constexpr int kStages = 98304 / kStageBytes;            // 5 (16 tokens) to 3 (128)
+  static constexpr int kCtas = kT <= 128 ? 2 : 1;                // an SM
+  static constexpr int kStages = 196608 / kCtas / kStageBytes;   // 5 (16 tokens) to 3 (128); 4
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + (2 * kStages + 1) * 8 + 16;
   static constexpr uint32_t kTmemCols = kT < 32 ? 32 : kT;
   static_assert(kT * 128 * 4 <= kStages * kStageBytes, "the partial sums reuse the ring");
-  static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs an SM");
+  static_assert(kCtas * (kSmemBytes + 1024) <= 233472, "shared memory of an SM");
 };
 
 struct SkinnyArgs {
@@ -147,7 +148,7 @@ __device__ __forceinline__ void skinny_finish(const LinearArgs& a, const HeadArg
 }
 
 template <bool kBF16, int kT, bool kQkv>
-__global__ void __launch_bounds__(kSkinnyThreads, 2)
+__global__ void __launch_bounds__(kSkinnyThreads, SkinnyLin<kT>::kCtas)
 linear_skinny_kernel(const __grid_constant__ PairLinMaps maps,
                      const __grid_constant__ SkinnyArgs args) {
   using S = SkinnyLin<kT>;
@@ -278,16 +279,33 @@ linear_skinny_kernel(const __grid_constant__ PairLinMaps maps,
   if (!skip && !*abort_flag) {
     const int tokens = min(kT, args.rows - t0);
     const uint32_t mine = smem_u32(part) + (uint32_t)lane * 16u;
-    for (int t = rank + splits * warp; t < tokens; t += splits * (kSkinnyThreads / 32)) {
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int r = 0; r < splits; ++r) {
-        const float4 v = ld_cluster_f4(mapa_shared(mine + (uint32_t)t * 512u, (uint32_t)r));
-        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    const bool run_on = args.rows != a.N;              // rows go through all branches
+    // two tokens at a time, all their partial sums in flight together
+    const int step = splits * (kSkinnyThreads / 32);
+    for (int t = rank + splits * warp; t < tokens; t += 2 * step) {
+      const bool two = t + step < tokens;
+      float4 v[2][8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        if (r < splits) {
+          const uint32_t peer = mapa_shared(mine, (uint32_t)r);
+          v[0][r] = ld_cluster_f4(peer + (uint32_t)t * 512u);
+          if (two) v[1][r] = ld_cluster_f4(peer + (uint32_t)(t + step) * 512u);
+        }
       }
-      const int row = t0 + t;
-      const int b = args.rows == a.N ? z : row / a.N;
-      skinny_finish<kBF16, kQkv>(a, args.head, s, b, row - (args.rows == a.N ? 0 : b * a.N),
-                                 c0 + 4 * lane);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (i == 1 && !two) break;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < splits) {
+            s.x += v[i][r].x; s.y += v[i][r].y; s.z += v[i][r].z; s.w += v[i][r].w;
+          }
+        const int row = t0 + t + i * step;
+        const int b = run_on ? row / a.N : z;
+        skinny_finish<kBF16, kQkv>(a, args.head, s, b, run_on ? row - b * a.N : row, c0 + 4 * lane);
+      }
     }
   }
   // no CTA leaves while its partial sums may still be read

@@ -16,9 +16,6 @@
 #include "linear_simt.cuh"
 #include "linear_skinny.cuh"
 #include "norm_rope.cuh"
-#ifndef LIN_BIG
-#define LIN_BIG 1000000
-#endif
 
 namespace tara {
 namespace {
@@ -139,14 +136,19 @@ int encode_weights(const DeviceInfo& dev, CUtensorMap* map, tara_dtype dt, const
   return encode_map(dev, map, dt, w, 2, dims, strides, box_rows);
 }
 
-template <bool kBF16, int BN, int kSubs, bool kQkv>
+template <bool kBF16, int BN, int kSubs, int kEpi>
 struct PairLauncher {
   static int allow(const DeviceInfo& dev) {
     static std::mutex mu;
     static uint64_t done = 0;   // one bit per device
     std::lock_guard<std::mutex> lock(mu);
     if (done >> dev.index & 1) return TARA_OK;
-    if (cudaFuncSetAttribute(linear_pair_kernel<kBF16, BN, kSubs, kQkv>,
+    // the kernel's register split draws on exactly this many registers a thread
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, linear_pair_kernel<kBF16, BN, kSubs, kEpi>) != cudaSuccess ||
+        fa.numRegs != kPairLinRegs)
+      return TARA_ERR_CUDA;
+    if (cudaFuncSetAttribute(linear_pair_kernel<kBF16, BN, kSubs, kEpi>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              PairLin<BN, kSubs>::kSmemBytes) != cudaSuccess)
       return TARA_ERR_CUDA;
@@ -169,7 +171,7 @@ struct PairLauncher {
     p.group = 8 / kSubs;
     const long long tiles = (long long)a.B * p.m_tiles * p.n_tiles;
     const long long clusters = std::min<long long>(tiles, std::max(1, dev.sms / 2));
-    linear_pair_kernel<kBF16, BN, kSubs, kQkv>
+    linear_pair_kernel<kBF16, BN, kSubs, kEpi>
         <<<(unsigned)(2 * clusters), kPairLinThreads, PairLin<BN, kSubs>::kSmemBytes, stream>>>(maps, p);
     return launched();
   }
@@ -195,8 +197,13 @@ void merge_branches(LinearArgs* a) {
 template <bool kBF16, int BN, int kSubs>
 int launch_pair(const DeviceInfo& dev, const PairLinArgs& p, bool heads, tara_dtype dt,
                 cudaStream_t stream) {
-  return heads ? PairLauncher<kBF16, BN, kSubs, true>::launch(dev, p, dt, stream)
-               : PairLauncher<kBF16, BN, kSubs, false>::launch(dev, p, dt, stream);
+  if (heads) return PairLauncher<kBF16, BN, kSubs, kEpiHeads>::launch(dev, p, dt, stream);
+  switch (p.lin.act) {
+    case 1: return PairLauncher<kBF16, BN, kSubs, 1>::launch(dev, p, dt, stream);
+    case 2: return PairLauncher<kBF16, BN, kSubs, 2>::launch(dev, p, dt, stream);
+    case 3: return PairLauncher<kBF16, BN, kSubs, 3>::launch(dev, p, dt, stream);
+    default: return PairLauncher<kBF16, BN, kSubs, 0>::launch(dev, p, dt, stream);
+  }
 }
 
 template <bool kBF16, int kT, bool kQkv>
@@ -223,9 +230,9 @@ int launch_skinny(const DeviceInfo& dev, SkinnyArgs p, int zs, tara_dtype dt, cu
       (rc = encode_weights(dev, &maps.w, dt, a.w, a.C, a.K, 128)) != TARA_OK)
     return rc;
   const long long c_tiles = ((long long)a.C + 127) / 128, t_tiles = ((long long)p.rows + kT - 1) / kT;
-  // K is split so that the CTAs fill whole rounds of the 2 an SM that run together; a CTA's
+  // K is split so that the CTAs fill whole rounds of those that run together; a CTA's
   // start and end cost about as much as 8 of its K steps
-  const long long tiles = c_tiles * t_tiles * zs, slots = 2LL * dev.sms, steps = (a.K + 63) / 64;
+  const long long tiles = c_tiles * t_tiles * zs, slots = (long long)S::kCtas * dev.sms, steps = (a.K + 63) / 64;
   long long best = 0;
   for (int s = 1; s <= 8 && s <= steps; s *= 2) {
     const long long cost = (tiles * s + slots - 1) / slots * ((steps + s - 1) / s + 8);
@@ -256,14 +263,12 @@ int launch_skinny_rows(const DeviceInfo& dev, const SkinnyArgs& p, int zs, tara_
   if (p.rows <= 16) return launch_skinny<kBF16, 16, kQkv>(dev, p, zs, dt, stream);
   if (p.rows <= 32) return launch_skinny<kBF16, 32, kQkv>(dev, p, zs, dt, stream);
   if (p.rows <= 64) return launch_skinny<kBF16, 64, kQkv>(dev, p, zs, dt, stream);
-  return launch_skinny<kBF16, 128, kQkv>(dev, p, zs, dt, stream);
+  if (p.rows <= 128) return launch_skinny<kBF16, 128, kQkv>(dev, p, zs, dt, stream);
+  return launch_skinny<kBF16, 256, kQkv>(dev, p, zs, dt, stream);
 }
 
 // Rows up to which the weight-streaming kernel is taken.
-#ifndef SKINNY_ROWS
-#define SKINNY_ROWS 256
-#endif
-constexpr long long kSkinnyRows = SKINNY_ROWS;
+constexpr long long kSkinnyRows = 256;
 
 // head: the norm and rotation of a projection's q and k, or nullptr.
 int run_linear(LinearArgs a, const HeadArgs* head, tara_dtype dt, cudaStream_t stream) {
@@ -302,10 +307,25 @@ int run_linear(LinearArgs a, const HeadArgs* head, tara_dtype dt, cudaStream_t s
   PairLinArgs p{};
   p.lin = a;
   if (head) p.head = *head;
-  // 256 columns a tile halve the loads of x per product, two sub-tiles those of W; the smaller
-  // tiles where the larger would leave SM pairs idle
+  // Tile size by the estimated cycles of a cluster's rounds.  A 64-column K step takes 512 (256 x
+  // 256) or 1,024 cycles (512 x 256) of the tensor cores; 256 x 128 needs 256, but its 24 KB of
+  // operands an SM arrive at about 64 bytes a cycle, so 384.  What a round costs beyond its
+  // products (filling the ring, the last tile's epilogue) counts as 8 K steps.
   const int pairs = std::max(1, dev.sms / 2);
-  const int size = tiles128 / 4 >= LIN_BIG * pairs ? 2 : (tiles128 / 2 >= pairs ? 1 : 0);
+  const long long k_steps = ((long long)a.K + 63) / 64;
+  auto cycles = [&](int rows, int cols, long long step) {
+    const long long tiles = (long long)a.B * (((long long)a.N + rows - 1) / rows) *
+                            (((long long)a.C + cols - 1) / cols);
+    return (tiles + pairs - 1) / pairs * k_steps * step + 8 * step;
+  };
+  const long long c256 = cycles(256, 256, 512), c128 = cycles(256, 128, 384);
+  int size = c128 < c256 ? 0 : 1;
+  // 512 x 256 reads a quarter less through L2 than 256 x 256, but its accumulators fill tensor
+  // memory, so part of every epilogue is exposed (about 7,000 cycles).  Long calls run at the
+  // power cap, where the saved traffic counts for more: 107,126 x 7,168 -> 7,168 back to back
+  // takes 8.7 ms against 9.3; with 1,024 input columns the exposed epilogue loses (1.05 against
+  // 0.69 ms).
+  if (size == 1 && k_steps >= 64 && tiles128 / 2 >= 32LL * pairs) size = 2;
   if (dt == TARA_BF16) {
     if (size == 2) return launch_pair<true, 256, 2>(dev, p, heads, dt, stream);
     if (size == 1) return launch_pair<true, 256, 1>(dev, p, heads, dt, stream);
