@@ -59,20 +59,32 @@ def pack_token_positions(grids: Sequence[TokenGrid], n_axes: int = 3) -> np.ndar
 # ---------------------------------------------------------------------------------------
 # marshalling
 # ---------------------------------------------------------------------------------------
+_DTYPES = {}   # torch dtype -> tara_dtype, filled on first use (torch is imported late)
+
+
+def _dtype(t) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        code = _DTYPES[t.dtype] = _dtype_code(t)
+    return code
+
+
 def _view(t) -> TaraView:
     """View of [B][H][N][D], [B][N][C] or [N][C] (any strides, last dimension contiguous)."""
-    nd = t.dim()
     shape, stride = t.shape, t.stride()
+    nd = len(stride)
     if nd < 2 or nd > 4:
         raise ValueError("expected [B][H][N][D], [B][N][C] or [N][C]")
     if stride[-1] != 1 and shape[-1] != 1:
         raise ValueError("the last dimension must be contiguous")
-    v = TaraView()
-    v.ptr, v.dtype = t.data_ptr(), _dtype_code(t)
-    v.N, v.D, v.stride_n = shape[-2], shape[-1], stride[-2]
-    v.B, v.stride_b = (shape[0], stride[0]) if nd > 2 else (1, 0)
-    v.H, v.stride_h = (shape[1], stride[1]) if nd > 3 else (1, 0)
-    return v
+    if max(shape) > 0x7fffffff:
+        raise ValueError("a dimension is longer than 2^31 - 1")
+    if nd == 3:
+        return TaraView(t.data_ptr(), _dtype(t), shape[0], 1, shape[1], shape[2], stride[0], 0,
+                        stride[1])
+    if nd == 4:
+        return TaraView(t.data_ptr(), _dtype(t), *shape, *stride[:3])
+    return TaraView(t.data_ptr(), _dtype(t), 1, 1, shape[0], shape[1], 0, 0, stride[0])
 
 
 def _vector(t, name: str, like, *shapes) -> Optional[int]:
@@ -88,32 +100,35 @@ def _vector(t, name: str, like, *shapes) -> Optional[int]:
 
 
 def _same_device(like, *tensors) -> None:
+    device = like.device
     for t in tensors:
-        if t is not None and t.device != like.device:
+        if t is not None and t.device != device:
             raise ValueError("all tensors must be on one device")
 
 
-@contextlib.contextmanager
-def _launching(device, stream):
-    """The stream handle of a call, with `device` (and a stream that was given) current."""
+def _elsewhere(t, stream):
+    """None when a call on t runs where the caller is (its current device and stream);
+    otherwise a context that makes t's device, and the stream that was given, current."""
     import torch
-    with torch.cuda.device(device):
-        if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-        else:
-            with torch.cuda.stream(stream):
-                yield ctypes.c_void_p(stream.cuda_stream)
+    if not t.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    if stream is None and torch.cuda.current_device() == t.device.index:
+        return None
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(t.device))
+    if stream is not None:
+        stack.enter_context(torch.cuda.stream(stream))
+    return stack
+
+
+def _current_stream(t) -> int:
+    import torch
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _check(rc: int, what: str) -> None:
     if rc != 0:
         raise TaraError(rc, what)
-
-
-def _cuda_only(*tensors) -> None:
-    for t in tensors:
-        if not t.is_cuda:
-            raise ValueError("expected CUDA tensors")
 
 
 # ---------------------------------------------------------------------------------------
@@ -124,27 +139,27 @@ def rope_table(pos, dims: Sequence[int], theta=10000.0, out=None, stream=None):
     [..., N, axes] (float32, contiguous).  dims: columns of each axis; theta: one base or one
     per axis."""
     import torch
-    _cuda_only(pos)
+    away = _elsewhere(pos, stream)
+    if away is not None:
+        with away:
+            return rope_table(pos, dims, theta, out)
     if pos.dtype != torch.float32 or not pos.is_contiguous() or pos.dim() < 2:
         raise ValueError("pos must be a contiguous float32 [..., N, axes] tensor")
     n_axes = len(dims)
     thetas = list(theta) if isinstance(theta, (list, tuple)) else [theta] * n_axes
     if pos.shape[-1] != n_axes or len(thetas) != n_axes or n_axes > ROPE_MAX_AXES:
         raise ValueError("pos, dims and theta must agree on the axes (at most %d)" % ROPE_MAX_AXES)
-    r = TaraRope()
-    r.n_axes = n_axes
-    for a in range(n_axes):
-        r.dim[a], r.theta[a] = int(dims[a]), float(thetas[a])
-    shape = tuple(pos.shape[:-1]) + (sum(int(d) for d in dims) // 2, 2)
-    with _launching(pos.device, stream) as s:
-        if out is None:
-            out = torch.empty(shape, dtype=torch.float32, device=pos.device)
-        elif tuple(out.shape) != shape or out.dtype != torch.float32 or not out.is_contiguous():
-            raise ValueError("out must be contiguous float32 of shape %s" % (shape,))
+    r = TaraRope(n_axes, tuple(dims), tuple(thetas))
+    shape = tuple(pos.shape[:-1]) + (sum(dims) // 2, 2)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=pos.device)
+    elif tuple(out.shape) != shape or out.dtype != torch.float32 or not out.is_contiguous():
+        raise ValueError("out must be contiguous float32 of shape %s" % (shape,))
+    else:
         _same_device(pos, out)
-        _check(load_library().tara_rope_table(pos.data_ptr(), pos.numel() // max(1, n_axes),
-                                              ctypes.byref(r), out.data_ptr(), s),
-               "tara_rope_table")
+    _check(load_library().tara_rope_table(pos.data_ptr(), pos.numel() // max(1, n_axes),
+                                          ctypes.byref(r), out.data_ptr(), _current_stream(pos)),
+           "tara_rope_table")
     return out
 
 
@@ -183,22 +198,27 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, eps: float = 1e-6, nor
     q_out / k_out are given (an output may be its own input).  k = None processes q alone and
     returns one tensor."""
     import torch
-    _cuda_only(q)
+    away = _elsewhere(q, stream)
+    if away is not None:
+        with away:
+            return qk_norm_rope(q, k, q_weight, k_weight, eps, norm, table, pairing, q_out, k_out)
     _same_device(q, k, q_out, k_out)
     if q.dim() != 4:
         raise ValueError("q must be [B][H][N][D]")
-    B, H, N, D = (int(x) for x in q.shape)
+    if k is None and (k_out is not None or k_weight is not None):
+        raise ValueError("k_out and k_weight need k")
+    B, H, N, D = q.shape
     p = _norm_rope_struct(q, H, N, D, B, q_weight, k_weight, eps, norm, table, pairing)
-    with _launching(q.device, stream) as s:
-        if q_out is None:
-            q_out = torch.empty((B, H, N, D), dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
+    if q_out is None:
+        q_out = torch.empty((B, H, N, D), dtype=q.dtype, device=q.device)
+    kv = ko = None
+    if k is not None:
+        if k_out is None:
             k_out = torch.empty((B, H, N, D), dtype=q.dtype, device=q.device)
-        if k is None and k_out is not None:
-            raise ValueError("k_out without k")
-        ref = lambda t: ctypes.byref(_view(t)) if t is not None else None
-        _check(load_library().tara_qk_norm_rope(ref(q), ref(k), ctypes.byref(p), ref(q_out),
-                                                ref(k_out), s), "tara_qk_norm_rope")
+        kv, ko = ctypes.byref(_view(k)), ctypes.byref(_view(k_out))
+    _check(load_library().tara_qk_norm_rope(ctypes.byref(_view(q)), kv, ctypes.byref(p),
+                                            ctypes.byref(_view(q_out)), ko, _current_stream(q)),
+           "tara_qk_norm_rope")
     return q_out if k is None else (q_out, k_out)
 
 
@@ -211,39 +231,37 @@ def linear(x, w, bias=None, act: Optional[str] = None, gate=None, residual=None,
     "gelu_tanh" or "silu"; residual: columns of out in any of the layouts.  The result is
     [N][C_out] or [B][N][C_out], or [B][heads][N][C_out/heads] when heads is given."""
     import torch
-    _cuda_only(x)
-    _same_device(x, w, bias, gate, residual, out)
+    away = _elsewhere(x, stream)
+    if away is not None:
+        with away:
+            return linear(x, w, bias, act, gate, residual, heads, out)
+    _same_device(x, w, residual, out)
     if act not in ACTS:
         raise ValueError("act must be one of %s" % sorted(a for a in ACTS if a))
     xv = _view(x)
     if w.dim() != 2 or w.shape[1] != xv.H * xv.D or w.dtype != x.dtype or not w.is_contiguous():
         raise ValueError("w must be contiguous [C_out][C_in] of x's dtype")
-    B, N, C = xv.B, xv.N, int(w.shape[0])
-    e = TaraEpilogue()
-    e.bias = _vector(bias, "bias", x, (C,))
-    e.act = ACTS[act]
-    e.gate = _vector(gate, "gate", x, (C,), (B, C))
-    e.gate_stride = C if gate is not None and gate.dim() == 2 and B > 1 else 0
-    rv = None
-    if residual is not None:
-        rv = _view(residual)
-        e.residual = ctypes.pointer(rv)
+    B, N, C = xv.B, xv.N, w.shape[0]
     if heads is not None and (heads < 1 or C % heads != 0):
         raise ValueError("heads must divide the output columns")
-    with _launching(x.device, stream) as s:
-        if out is None:
-            if heads is not None:
-                shape = (B, heads, N, C // heads)
-            else:
-                shape = (N, C) if x.dim() == 2 else (B, N, C)
-            out = torch.empty(shape, dtype=x.dtype, device=x.device)
-        elif heads is not None and (out.dim() != 4 or out.shape[1] != heads):
-            raise ValueError("out must be [B][heads][N][D]")
-        yv = _view(out)
-        if yv.H * yv.D != C:
-            raise ValueError("out must have %d columns" % C)
-        _check(load_library().tara_linear(ctypes.byref(xv), w.data_ptr(), ctypes.byref(e),
-                                          ctypes.byref(yv), s), "tara_linear")
+    e = TaraEpilogue(_vector(bias, "bias", x, (C,)), ACTS[act],
+                     _vector(gate, "gate", x, (C,), (B, C)),
+                     C if gate is not None and gate.dim() == 2 and B > 1 else 0)
+    if residual is not None:
+        e.residual = ctypes.pointer(_view(residual))
+    if out is None:
+        if heads is not None:
+            shape = (B, heads, N, C // heads)
+        else:
+            shape = (N, C) if x.dim() == 2 else (B, N, C)
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    elif heads is not None and (out.dim() != 4 or out.shape[1] != heads):
+        raise ValueError("out must be [B][heads][N][D]")
+    yv = _view(out)
+    if yv.H * yv.D != C:
+        raise ValueError("out must have %d columns" % C)
+    _check(load_library().tara_linear(ctypes.byref(xv), w.data_ptr(), ctypes.byref(e),
+                                      ctypes.byref(yv), _current_stream(x)), "tara_linear")
     return out
 
 
@@ -256,12 +274,15 @@ def qkv_project(x, w, heads: int, bias=None, q_weight=None, k_weight=None, eps: 
     x: [N][C_in], [B][N][C_in] or [B][H][N][D]; w: [3*heads*D][C_in]; out: three tensors or
     views [B][heads][N][D] to write, for instance rows of the packed sequence's q, k, v."""
     import torch
-    _cuda_only(x)
-    _same_device(x, w, bias)
+    away = _elsewhere(x, stream)
+    if away is not None:
+        with away:
+            return qkv_project(x, w, heads, bias, q_weight, k_weight, eps, norm, table, pairing, out)
+    _same_device(x, w)
     xv = _view(x)
     if w.dim() != 2 or w.shape[1] != xv.H * xv.D or w.dtype != x.dtype or not w.is_contiguous():
         raise ValueError("w must be contiguous [3*heads*D][C_in] of x's dtype")
-    rows = int(w.shape[0])
+    rows = w.shape[0]
     if heads < 1 or rows % (3 * heads) != 0:
         raise ValueError("w must have 3*heads*D rows")
     B, N, D = xv.B, xv.N, rows // (3 * heads)
@@ -272,14 +293,12 @@ def qkv_project(x, w, heads: int, bias=None, q_weight=None, k_weight=None, eps: 
     elif q_weight is not None or k_weight is not None:
         raise ValueError("weights are only used with the norm")
     bias_ptr = _vector(bias, "bias", x, (rows,))
-    with _launching(x.device, stream) as s:
-        if out is None:
-            out = tuple(torch.empty((B, heads, N, D), dtype=x.dtype, device=x.device)
-                        for _ in range(3))
-        q, k, v = out
-        _same_device(x, q, k, v)
-        views = [_view(t) for t in (q, k, v)]
-        _check(load_library().tara_qkv_project(
-            ctypes.byref(xv), w.data_ptr(), bias_ptr, p, *(ctypes.byref(t) for t in views), s),
-            "tara_qkv_project")
+    if out is None:
+        out = tuple(torch.empty((B, heads, N, D), dtype=x.dtype, device=x.device)
+                    for _ in range(3))
+    q, k, v = out
+    _same_device(x, q, k, v)
+    _check(load_library().tara_qkv_project(
+        ctypes.byref(xv), w.data_ptr(), bias_ptr, p, ctypes.byref(_view(q)),
+        ctypes.byref(_view(k)), ctypes.byref(_view(v)), _current_stream(x)), "tara_qkv_project")
     return q, k, v
