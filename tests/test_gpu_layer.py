@@ -236,6 +236,11 @@ LINEAR_CASES = [
     (3, 70, 129, 66, "fp32", 3, "r", None, 2),
     (1, 5, 2000, 300, "fp32", 0, "bG", None, None),
     (2, 500, 250, 404, "fp32", 0, "bgr", "gelu", None),
+    (1, 1500, 131, 1410, "fp32", 0, "bgr", "silu", None),
+    (2, 8, 259, 77, "fp32", 7, "bgr", "gelu_tanh", 7),
+    (3, 2, 33, 5, "fp32", 0, "g", None, None),
+    (1, 3, 640, 129, "fp32", 10, "r", None, 3),
+    (2, 9, 1000, 64, "fp32", 8, "b", None, 2),
 ]
 
 

@@ -273,11 +273,29 @@ constexpr long long kSkinnyRows = 256;
 // head: the norm and rotation of a projection's q and k, or nullptr.
 int run_linear(LinearArgs a, const HeadArgs* head, tara_dtype dt, cudaStream_t stream) {
   if (dt == TARA_FP32) {
-    const long long gx = ((long long)a.N + kSimtLinTile - 1) / kSimtLinTile;
-    const long long gy = ((long long)a.C + kSimtLinTile - 1) / kSimtLinTile;
-    if (gy > 65535) return TARA_ERR_TOO_LARGE;
-    const dim3 grid((unsigned)gx, (unsigned)gy, (unsigned)a.B);
-    linear_simt_kernel<float><<<grid, kSimtLinThreads, 0, stream>>>(a);
+    if (a.N <= kSimtRows) {
+      const int cols_cta = kSimtLinThreads / 32 * kRowsCols;
+      const dim3 grid((unsigned)(((long long)a.C + cols_cta - 1) / cols_cta), (unsigned)a.B);
+      if (a.N == 1)
+        linear_simt_rows_kernel<1><<<grid, kSimtLinThreads, 0, stream>>>(a);
+      else if (a.N == 2)
+        linear_simt_rows_kernel<2><<<grid, kSimtLinThreads, 0, stream>>>(a);
+      else if (a.N <= 4)
+        linear_simt_rows_kernel<4><<<grid, kSimtLinThreads, 0, stream>>>(a);
+      else
+        linear_simt_rows_kernel<kSimtRows><<<grid, kSimtLinThreads, 0, stream>>>(a);
+      return launched();
+    }
+    auto tiles = [&a](long long m) { return dim3((unsigned)((a.N + m - 1) / m),
+                                                 (unsigned)((a.C + m - 1) / m), (unsigned)a.B); };
+    // the large tiles as soon as they give every other SM one
+    const dim3 big = tiles(128), small = tiles(32);
+    const bool large = (long long)big.x * big.y * big.z >= 74;
+    if ((large ? big.y : small.y) > 65535) return TARA_ERR_TOO_LARGE;
+    if (large)
+      linear_simt_kernel<128, 16><<<big, kSimtLinThreads, 0, stream>>>(a);
+    else
+      linear_simt_kernel<32, 64><<<small, kSimtLinThreads, 0, stream>>>(a);
     return launched();
   }
   DeviceInfo dev;
