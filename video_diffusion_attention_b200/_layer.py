@@ -91,18 +91,19 @@ def _vector(t, name: str, like, *shapes) -> Optional[int]:
     """Pointer of an optional contiguous parameter of one of the given shapes."""
     if t is None:
         return None
-    if tuple(t.shape) not in shapes or not t.is_contiguous():
+    if t.shape not in shapes or not t.is_contiguous():
         raise ValueError("%s must be contiguous of shape %s" % (name, " or ".join(map(str, shapes))))
     if t.dtype != like.dtype:
         raise TypeError("%s must have the tensors' dtype" % name)
-    _same_device(like, t)
+    if t.get_device() != like.get_device():
+        raise ValueError("all tensors must be on one device")
     return t.data_ptr()
 
 
 def _same_device(like, *tensors) -> None:
-    device = like.device
+    device = like.get_device()
     for t in tensors:
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != device:
             raise ValueError("all tensors must be on one device")
 
 
@@ -112,7 +113,7 @@ def _elsewhere(t, stream):
     import torch
     if not t.is_cuda:
         raise ValueError("expected CUDA tensors")
-    if stream is None and torch.cuda.current_device() == t.device.index:
+    if stream is None and torch.cuda.current_device() == t.get_device():
         return None
     stack = contextlib.ExitStack()
     stack.enter_context(torch.cuda.device(t.device))
@@ -121,9 +122,16 @@ def _elsewhere(t, stream):
     return stack
 
 
+_raw_stream = None   # device index -> handle of its current stream
+
+
 def _current_stream(t) -> int:
-    import torch
-    return torch.cuda.current_stream(t.device).cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(t.get_device())
 
 
 def _check(rc: int, what: str) -> None:
@@ -152,7 +160,7 @@ def rope_table(pos, dims: Sequence[int], theta=10000.0, out=None, stream=None):
     r = TaraRope(n_axes, tuple(dims), tuple(thetas))
     shape = tuple(pos.shape[:-1]) + (sum(dims) // 2, 2)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=pos.device)
+        out = pos.new_empty(shape)
     elif tuple(out.shape) != shape or out.dtype != torch.float32 or not out.is_contiguous():
         raise ValueError("out must be contiguous float32 of shape %s" % (shape,))
     else:
@@ -164,29 +172,31 @@ def rope_table(pos, dims: Sequence[int], theta=10000.0, out=None, stream=None):
 
 
 def _norm_rope_struct(like, H, N, D, B, q_weight, k_weight, eps, norm, table, pairing):
-    p = TaraNormRope()
-    if pairing not in PAIRINGS:
+    code = PAIRINGS.get(pairing)
+    if code is None:
         raise ValueError("pairing must be one of %s" % sorted(PAIRINGS))
-    p.norm, p.eps, p.pairing = int(bool(norm)), eps, PAIRINGS[pairing]
+    qw = kw = None
+    stride = 0
     if norm:
-        per_head = [w.dim() == 2 for w in (q_weight, k_weight) if w is not None]
-        if per_head and any(per_head) != all(per_head):
+        if q_weight is not None and k_weight is not None and q_weight.dim() != k_weight.dim():
             raise ValueError("q_weight and k_weight must both be [D] or both [H][D]")
-        p.q_weight = _vector(q_weight, "q_weight", like, (D,), (H, D))
-        p.k_weight = _vector(k_weight, "k_weight", like, (D,), (H, D))
-        p.weight_head_stride = D if per_head and per_head[0] else 0
+        qw = _vector(q_weight, "q_weight", like, (D,), (H, D))
+        kw = _vector(k_weight, "k_weight", like, (D,), (H, D))
+        one = q_weight if q_weight is not None else k_weight
+        stride = D if one is not None and one.dim() == 2 else 0
     elif q_weight is not None or k_weight is not None:
         raise ValueError("weights are only used with the norm")
-    if table is not None:
-        import torch
-        if table.dtype != torch.float32 or not table.is_contiguous() or table.dim() not in (3, 4):
-            raise ValueError("table must be a contiguous float32 [N][R/2][2] or [B][N][R/2][2]")
-        if table.shape[-3] != N or table.shape[-1] != 2 or (table.dim() == 4 and table.shape[0] != B):
-            raise ValueError("table does not match the tokens")
-        _same_device(like, table)
-        p.table, p.rot_dim = table.data_ptr(), 2 * int(table.shape[-2])
-        p.table_batch_stride = table.stride(0) if table.dim() == 4 and B > 1 else 0
-    return p
+    if table is None:
+        return TaraNormRope(1 if norm else 0, eps, qw, kw, stride, None, 0, 0, code)
+    import torch
+    shape = table.shape
+    if table.dtype != torch.float32 or not table.is_contiguous() or len(shape) not in (3, 4):
+        raise ValueError("table must be a contiguous float32 [N][R/2][2] or [B][N][R/2][2]")
+    if shape[-3] != N or shape[-1] != 2 or (len(shape) == 4 and shape[0] != B):
+        raise ValueError("table does not match the tokens")
+    _same_device(like, table)
+    return TaraNormRope(1 if norm else 0, eps, qw, kw, stride, table.data_ptr(),
+                        table.stride(0) if len(shape) == 4 and B > 1 else 0, 2 * shape[-2], code)
 
 
 def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, eps: float = 1e-6, norm: bool = True,
@@ -197,7 +207,6 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, eps: float = 1e-6, nor
     q, k: [B][H][N][D] views with any strides; the outputs are new contiguous tensors unless
     q_out / k_out are given (an output may be its own input).  k = None processes q alone and
     returns one tensor."""
-    import torch
     away = _elsewhere(q, stream)
     if away is not None:
         with away:
@@ -210,11 +219,11 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, eps: float = 1e-6, nor
     B, H, N, D = q.shape
     p = _norm_rope_struct(q, H, N, D, B, q_weight, k_weight, eps, norm, table, pairing)
     if q_out is None:
-        q_out = torch.empty((B, H, N, D), dtype=q.dtype, device=q.device)
+        q_out = q.new_empty((B, H, N, D))
     kv = ko = None
     if k is not None:
         if k_out is None:
-            k_out = torch.empty((B, H, N, D), dtype=q.dtype, device=q.device)
+            k_out = q.new_empty((B, H, N, D))
         kv, ko = ctypes.byref(_view(k)), ctypes.byref(_view(k_out))
     _check(load_library().tara_qk_norm_rope(ctypes.byref(_view(q)), kv, ctypes.byref(p),
                                             ctypes.byref(_view(q_out)), ko, _current_stream(q)),
@@ -230,7 +239,6 @@ def linear(x, w, bias=None, act: Optional[str] = None, gate=None, residual=None,
     is); w: [C_out][C_in]; bias [C_out]; gate [C_out] or [B][C_out]; act: None, "gelu",
     "gelu_tanh" or "silu"; residual: columns of out in any of the layouts.  The result is
     [N][C_out] or [B][N][C_out], or [B][heads][N][C_out/heads] when heads is given."""
-    import torch
     away = _elsewhere(x, stream)
     if away is not None:
         with away:
@@ -254,7 +262,7 @@ def linear(x, w, bias=None, act: Optional[str] = None, gate=None, residual=None,
             shape = (B, heads, N, C // heads)
         else:
             shape = (N, C) if x.dim() == 2 else (B, N, C)
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(shape)
     elif heads is not None and (out.dim() != 4 or out.shape[1] != heads):
         raise ValueError("out must be [B][heads][N][D]")
     yv = _view(out)
@@ -273,7 +281,6 @@ def qkv_project(x, w, heads: int, bias=None, q_weight=None, k_weight=None, eps: 
 
     x: [N][C_in], [B][N][C_in] or [B][H][N][D]; w: [3*heads*D][C_in]; out: three tensors or
     views [B][heads][N][D] to write, for instance rows of the packed sequence's q, k, v."""
-    import torch
     away = _elsewhere(x, stream)
     if away is not None:
         with away:
@@ -294,8 +301,8 @@ def qkv_project(x, w, heads: int, bias=None, q_weight=None, k_weight=None, eps: 
         raise ValueError("weights are only used with the norm")
     bias_ptr = _vector(bias, "bias", x, (rows,))
     if out is None:
-        out = tuple(torch.empty((B, heads, N, D), dtype=x.dtype, device=x.device)
-                    for _ in range(3))
+        shape = (B, heads, N, D)
+        out = (x.new_empty(shape), x.new_empty(shape), x.new_empty(shape))
     q, k, v = out
     _same_device(x, q, k, v)
     _check(load_library().tara_qkv_project(
