@@ -6,6 +6,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "sm100_ptx.cuh"
+
 namespace tara {
 
 // A strided [B][H][N][D] view whose rows are indexed by column c = h * D + d.
@@ -31,54 +33,83 @@ struct LinearArgs {
   int* status;
 };
 
-// v/2 (1 + erf(v / sqrt 2)) as v Phi(v), with Phi from erfc(x) = t exp(-x^2 + P(t)),
-// t = 1 / (1 + x/2), x = |v| / sqrt 2: the form of Numerical Recipes' erfcc, P a polynomial of
-// degree 9 in t fitted to ln(erfc(x) exp(x^2) / t) on 0 <= x <= 10 by Lawson's iteration (largest
-// error 4.5e-8), in log2 units here.  The tail keeps its relative accuracy, and a branch-free
-// 16 operations replace a call of erff: with 1,024 input columns erff bounded the kernel.
-__device__ __forceinline__ float gelu_erf(float v) {
-  const float a = fabsf(v);
-  const float t = __fdividef(1.0f, fmaf(a, 0.35355339059f, 1.0f));
-  float p = 0.20514240860939026f;
-  p = fmaf(p, t, -0.96092289686203f);
-  p = fmaf(p, t, 1.6192750930786133f);
-  p = fmaf(p, t, -0.9395431876182556f);
-  p = fmaf(p, t, -0.1684969663619995f);
-  p = fmaf(p, t, 0.02914106659591198f);
-  p = fmaf(p, t, 0.040909137576818466f);
-  p = fmaf(p, t, 0.5596213340759277f);
-  p = fmaf(p, t, 1.440520167350769f);
-  p = fmaf(p, t, -1.8256460428237915f);
-  const float half_erfc = 0.5f * t * exp2f(fmaf(-0.72134752044448170f * v, v, p));
-  return v * (v < 0.0f ? half_erfc : 1.0f - half_erfc);
+// Activations on the fp32 accumulators (numbering of tara_act), two elements at a time in packed
+// fp32.  What bounds them in the epilogue is the special-function unit, 16 results a cycle and SM:
+// two reciprocals are taken as one, of the product (1.5 operations an element instead of 2;
+// operands are clamped so that the product stays finite and an infinity or NaN stays in its own
+// element), and the polynomial runs on packed FMAs.
+__device__ __forceinline__ uint64_t both(float c) { return f32x2_pack(c, c); }
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// Activations on the fp32 accumulator (numbering of tara_act).
-template <int kAct>
-__device__ __forceinline__ float activate(float v) {
-  if (kAct == 1) return gelu_erf(v);
-  if (kAct == 2) {
-    // v/2 (1 + tanh u) = v / (1 + exp(-2u))
-    const float u = 0.79788456080286536f * (v + 0.044715f * v * v * v);
-    return __fdividef(v, 1.0f + __expf(-2.0f * u));
-  }
-  if (kAct == 3) return __fdividef(v, 1.0f + __expf(-v));
-  return v;
+// v <- v / (1 + 2^x)
+__device__ __forceinline__ void logistic_pair(float& v0, float& v1, uint64_t x) {
+  float x0, x1, d0, d1;
+  f32x2_unpack(x, x0, x1);
+  f32x2_unpack(f32x2_add(f32x2_pack(ex2_approx(fminf(x0, 60.f)), ex2_approx(fminf(x1, 60.f))),
+                         both(1.f)), d0, d1);
+  const float r = rcp_approx(d0 * d1);
+  v0 *= r * d1;
+  v1 *= r * d0;
 }
-// In place on a thread's values; the branch on the activation is taken once.
-template <int kN>
-__device__ __forceinline__ void activate_all(float (&f)[kN], int act) {
-  if (act == 0) return;
-  if (act == 1) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) f[i] = activate<1>(f[i]);
-  } else if (act == 2) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) f[i] = activate<2>(f[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) f[i] = activate<3>(f[i]);
+
+template <int kAct>
+__device__ __forceinline__ void activate_pair(float& v0, float& v1) {
+  const uint64_t v = f32x2_pack(v0, v1);
+  if (kAct == 1) {
+    // v/2 (1 + erf(v / sqrt 2)) = v Phi(v), with Phi from erfc(x) = t exp(-x^2 + P(t)),
+    // t = 1 / (1 + x/2), x = |v| / sqrt 2: the form of Numerical Recipes' erfcc, P a polynomial
+    // of degree 9 in t fitted to ln(erfc(x) exp(x^2) / t) on 0 <= x <= 10 by Lawson's iteration
+    // (largest error 4.5e-8), in log2 units here.  The tail keeps its relative accuracy.
+    float d0, d1, e0, e1;
+    f32x2_unpack(f32x2_fma(f32x2_pack(fminf(fabsf(v0), 64.f), fminf(fabsf(v1), 64.f)),
+                           both(0.35355339059f), both(1.f)), d0, d1);
+    const float r = rcp_approx(d0 * d1);
+    const uint64_t t = f32x2_pack(r * d1, r * d0);
+    uint64_t p = f32x2_fma(t, both(0.20514240860939026f), both(-0.96092289686203f));
+    p = f32x2_fma(p, t, both(1.6192750930786133f));
+    p = f32x2_fma(p, t, both(-0.9395431876182556f));
+    p = f32x2_fma(p, t, both(-0.1684969663619995f));
+    p = f32x2_fma(p, t, both(0.02914106659591198f));
+    p = f32x2_fma(p, t, both(0.040909137576818466f));
+    p = f32x2_fma(p, t, both(0.5596213340759277f));
+    p = f32x2_fma(p, t, both(1.440520167350769f));
+    p = f32x2_fma(p, t, both(-1.8256460428237915f));
+    f32x2_unpack(f32x2_fma(f32x2_mul(v, v), both(-0.72134752044448170f), p), e0, e1);
+    float h0, h1;                                  // erfc / 2
+    f32x2_unpack(f32x2_mul(f32x2_mul(t, both(0.5f)), f32x2_pack(ex2_approx(e0), ex2_approx(e1))),
+                 h0, h1);
+    v0 *= v0 < 0.f ? h0 : 1.f - h0;
+    v1 *= v1 < 0.f ? h1 : 1.f - h1;
+  } else if (kAct == 2) {
+    // v/2 (1 + tanh u) = v / (1 + exp(-2u)), u = sqrt(2/pi) (v + 0.044715 v^3)
+    const uint64_t s = f32x2_fma(f32x2_mul(v, v), both(-0.10294324f), both(-2.30220819814f));
+    logistic_pair(v0, v1, f32x2_mul(v, s));
+  } else if (kAct == 3) {
+    logistic_pair(v0, v1, f32x2_mul(v, both(-1.44269504089f)));
   }
+}
+
+// In place on a thread's values.
+template <int kAct, int kN>
+__device__ __forceinline__ void activate(float (&f)[kN]) {
+  static_assert(kN % 2 == 0, "pairs");
+#pragma unroll
+  for (int i = 0; i < kN; i += 2) activate_pair<kAct>(f[i], f[i + 1]);
+}
+template <int kN>
+__device__ __forceinline__ void activate_any(float (&f)[kN], int act) {
+  if (act == 1) activate<1>(f);
+  else if (act == 2) activate<2>(f);
+  else if (act == 3) activate<3>(f);
 }
 
 }  // namespace tara

@@ -191,8 +191,7 @@ __device__ __forceinline__ void pair_linear(const PairWarp& w, PairLinearAhead& 
         for (int i = 0; i < 8; ++i) f[q * 8 + i] += t[i];
       }
     }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] = activate<kAct>(f[i]);
+    if (kAct != 0) activate<kAct>(f);
     if (ah.gate) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {

@@ -17,18 +17,26 @@ namespace tara {
 
 constexpr int kSimtLinThreads = 256;
 
+// The activations once more for single fp32 results, by CUDA's own functions.
+__device__ __forceinline__ float simt_activate(float v, int act) {
+  if (act == 1) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  if (act == 2) return v / (1.0f + expf(-1.59576912160573072f * (v + 0.044715f * v * v * v)));
+  if (act == 3) return v / (1.0f + expf(-v));
+  return v;
+}
+
 // act(acc + bias) * gate + residual -> y, one element.
 __device__ __forceinline__ void simt_finish(const LinearArgs& a, int b, long long n, int c,
                                             float acc) {
-  float v[1] = {acc};
-  if (a.bias) v[0] += static_cast<const float*>(a.bias)[c];
-  activate_all(v, a.act);
-  if (a.gate) v[0] *= static_cast<const float*>(a.gate)[b * a.gate_b + c];
+  float v = acc;
+  if (a.bias) v += static_cast<const float*>(a.bias)[c];
+  v = simt_activate(v, a.act);
+  if (a.gate) v *= static_cast<const float*>(a.gate)[b * a.gate_b + c];
   if (a.residual.ptr)
-    v[0] += static_cast<const float*>(a.residual.ptr)[row_offset(a.residual, b, n, c)];
+    v += static_cast<const float*>(a.residual.ptr)[row_offset(a.residual, b, n, c)];
   const int part = c < a.part_cols ? 0 : c / a.part_cols;
   const RowView& y = a.y[part];
-  static_cast<float*>(const_cast<void*>(y.ptr))[row_offset(y, b, n, c - part * a.part_cols)] = v[0];
+  static_cast<float*>(const_cast<void*>(y.ptr))[row_offset(y, b, n, c - part * a.part_cols)] = v;
 }
 
 template <int kM, int kK>

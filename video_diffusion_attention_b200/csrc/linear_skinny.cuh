@@ -85,7 +85,7 @@ __device__ __forceinline__ void skinny_finish(const LinearArgs& a, const HeadArg
     f[0] += t.x; f[1] += t.y; f[2] += t.z; f[3] += t.w;
   }
   if (!kQkv) {
-    activate_all(f, a.act);
+    activate_any(f, a.act);
     if (a.gate && ok) {
       const float4 t = load4<kBF16>(a.gate, b * a.gate_b + c);
       f[0] *= t.x; f[1] *= t.y; f[2] *= t.z; f[3] *= t.w;
