@@ -79,7 +79,7 @@ def test_rope_table_refuses_pointers_and_sizes(lib):
     assert lib.tara_rope_table(FAKE, 0, ref(r), FAKE2, None) == SHAPE
     assert lib.tara_rope_table(FAKE + 2, 10, ref(r), FAKE2, None) == ALIGN
     assert lib.tara_rope_table(FAKE, 10, ref(r), FAKE2 + 8, None) == ALIGN
-    assert lib.tara_rope_table(FAKE, 1 << 40, ref(r), FAKE2, None) == TOO_LARGE
+    assert lib.tara_rope_table(FAKE, 1 << 41, ref(r), FAKE2, None) == TOO_LARGE
     r.n_axes = 5
     assert lib.tara_rope_table(FAKE, 10, ref(r), FAKE2, None) == PARAM
 

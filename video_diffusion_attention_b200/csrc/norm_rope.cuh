@@ -167,31 +167,52 @@ __device__ __forceinline__ float2 turn_quarters(float2 sc, int q) {
 }
 
 // Write-bound (8 bytes a pair).  A thread keeps two neighbouring pairs (one 16-byte store) and
-// walks kSteps rows, so pair index, axis and frequency are set up once; the positions of a
-// CTA's rows are read through L1.
-template <int kSteps>
+// walks rows with the stride of the grid, kRopeBatch rows' positions in flight, so that pair
+// index, axis and frequency are set up once.  The frequencies pass through shared memory: read
+// by thread index from the kernel's arguments they are fetched one address at a time, which with
+// 8 rows a thread took half of the time.
+constexpr int kRopeBatch = 4;
+
 __global__ void __launch_bounds__(kRopeThreads)
 rope_table_kernel(const float* __restrict__ pos, long long n_rows,
                   const __grid_constant__ RopeFreqs fr, float4* __restrict__ table) {
+  __shared__ double s_freq[kRopeMaxPairs];
+  __shared__ uint8_t s_axis[kRopeMaxPairs];
+  for (int i = threadIdx.x; i < fr.n_pairs; i += kRopeThreads) {
+    s_freq[i] = fr.quarter_turns[i];
+    s_axis[i] = fr.axis[i];
+  }
+  __syncthreads();
   const int row_units = fr.n_pairs / 2;                   // 16-byte units of a row
-  const int rows_step = kRopeThreads / row_units;         // rows of one step
+  const int rows_step = kRopeThreads / row_units;         // rows of one step of a CTA
   const int r = threadIdx.x / row_units, u = threadIdx.x - r * row_units;
   if (r >= rows_step) return;
-  const double f0 = fr.quarter_turns[2 * u], f1 = fr.quarter_turns[2 * u + 1];
-  const int a0 = fr.axis[2 * u], a1 = fr.axis[2 * u + 1];
-  const long long row0 = (long long)blockIdx.x * rows_step * kSteps + r;
+  const double f0 = s_freq[2 * u], f1 = s_freq[2 * u + 1];
+  const float* p0 = pos + s_axis[2 * u];
+  const float* p1 = pos + s_axis[2 * u + 1];
+  const int n_axes = fr.n_axes;
+  const long long stride = (long long)gridDim.x * rows_step;
+  for (long long row0 = (long long)blockIdx.x * rows_step + r; row0 < n_rows;
+       row0 += kRopeBatch * stride) {
+    float x[kRopeBatch], y[kRopeBatch];
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const long long row = row0 + (long long)i * rows_step;
-    if (row >= n_rows) return;
-    const float* p = pos + row * fr.n_axes;
-    int q0, q1;
-    const float x0 = quarter_turn_remainder((double)p[a0], f0, q0);
-    const float x1 = quarter_turn_remainder((double)p[a1], f1, q1);
-    float2 sc[2];
-    sin_cos_small2(x0, x1, sc);
-    const float2 t0 = turn_quarters(sc[0], q0), t1 = turn_quarters(sc[1], q1);
-    table[row * row_units + u] = make_float4(t0.x, t0.y, t1.x, t1.y);
+    for (int i = 0; i < kRopeBatch; ++i) {
+      const long long row = min(row0 + i * stride, n_rows - 1);
+      x[i] = __ldg(p0 + row * n_axes);
+      y[i] = __ldg(p1 + row * n_axes);
+    }
+#pragma unroll
+    for (int i = 0; i < kRopeBatch; ++i) {
+      const long long row = row0 + i * stride;
+      if (row >= n_rows) break;
+      int q0, q1;
+      const float a0 = quarter_turn_remainder((double)x[i], f0, q0);
+      const float a1 = quarter_turn_remainder((double)y[i], f1, q1);
+      float2 sc[2];
+      sin_cos_small2(a0, a1, sc);
+      const float2 t0 = turn_quarters(sc[0], q0), t1 = turn_quarters(sc[1], q1);
+      table[row * row_units + u] = make_float4(t0.x, t0.y, t1.x, t1.y);
+    }
   }
 }
 

@@ -386,18 +386,12 @@ int tara_rope_table(const float* pos, int64_t n_rows, const tara_rope* rope, flo
       fr.quarter_turns[fr.n_pairs++] =
           std::pow(rope->theta[a], -2.0 * i / rope->dim[a]) * 0.63661977236758134308;   // 2/pi
     }
-  // eight rows a thread once that still gives every SM a few CTAs, one row otherwise
+  // one row a thread, up to the CTAs that run together (6 an SM)
   const long long rows_step = kRopeThreads / (fr.n_pairs / 2);
-  const bool many = n_rows >= rows_step * 8 * 148 * 4;
-  const long long rows_cta = rows_step * (many ? 8 : 1);
-  const long long grid = (n_rows - 1) / rows_cta + 1;
-  if (n_rows > ((int64_t)1 << 40) || grid > 0x7fffffffLL) return TARA_ERR_TOO_LARGE;
-  float4* t = reinterpret_cast<float4*>(table);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (many)
-    rope_table_kernel<8><<<(unsigned)grid, kRopeThreads, 0, st>>>(pos, n_rows, fr, t);
-  else
-    rope_table_kernel<1><<<(unsigned)grid, kRopeThreads, 0, st>>>(pos, n_rows, fr, t);
+  const long long grid = std::min<long long>((n_rows - 1) / rows_step + 1, 148 * 6);
+  if (n_rows > ((int64_t)1 << 40)) return TARA_ERR_TOO_LARGE;
+  rope_table_kernel<<<(unsigned)grid, kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+      pos, n_rows, fr, reinterpret_cast<float4*>(table));
   return launched();
 }
 
