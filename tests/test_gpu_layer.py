@@ -281,6 +281,22 @@ def test_linear_views_and_gaps(dtype, N):
     assert torch.equal(buf[keep], before[keep])
 
 
+@pytest.mark.parametrize("B,N,heads_in", [(1, 20000, 0), (2, 10300, 32)])
+def test_linear_of_a_long_sequence(B, N, heads_in):
+    # enough rounds of long products for the 512 x 256 tiles; sampled rows, the ragged end among
+    # them (20,000 rows end 32 rows into a tile: its second half does not exist)
+    K, C = 4096, 8192
+    x, w, o = linear_inputs(B, N, K, C, "bf16", heads_in, "bgr")
+    y = T.linear(x, w, act="silu", **o)
+    assert T.device_status() == 0
+    rows = torch.tensor([0, 1, 127, 128, 255, 256, 511, 512, N // 2, N - 33, N - 32, N - 1], device="cuda")
+    xs = x[:, :, rows] if heads_in else x[:, rows]
+    sampled = dict(o, residual=o["residual"][:, rows])
+    value, bound = linear_ref(xs, w, sampled, "silu")
+    close(y[:, rows], value, bound, "bf16")
+    assert bool(torch.isfinite(y).all())
+
+
 def test_linear_keeps_bad_rows_apart():
     # infinities and NaN of one token stay in its row
     for N in (6, 300):
@@ -355,6 +371,218 @@ def qkv_check(case):
             close(out[i][b], value, bound, dtype)
 
 
+@pytest.mark.parametrize("halves", [False, True])
+def test_qkv_project_of_a_long_sequence(halves):
+    # the 512 x 256 tiles; sampled rows
+    N, K, H, D = 20100, 4096, 21, 128
+    x = rand((1, N, K), "bf16", 51)
+    w = rand((3 * H * D, K), "bf16", 52, K ** -0.5)
+    bias = rand((3 * H * D,), "bf16", 53, 0.3)
+    wq = rand((D,), "bf16", 54, 0.2, 1.0)
+    table = table_for(N, (16, 56, 56), 55)
+    out = T.qkv_project(x, w, H, bias, wq, wq, table=table,
+                        pairing="halves" if halves else "interleaved")
+    assert T.device_status() == 0
+    rows = torch.tensor([0, 31, 32, 255, 256, 511, 512, N // 2, N - 132, N - 2, N - 1], device="cuda")
+    v, e = ref.product(np64(x[0, rows]), np64(w), np64(bias))
+    v, e = (a.reshape(len(rows), 3, H, D).transpose(1, 2, 0, 3) for a in (v, e))
+    for i in range(3):
+        value, bound = (v[i], e[i]) if i == 2 else ref.norm_rope(
+            v[i], np64(wq), float(np.float32(1e-6)), True, np64(table[rows]), halves, e[i])
+        close(out[i][0][:, rows], value, bound, "bf16")
+        assert bool(torch.isfinite(out[i]).all())
+
+
 @pytest.mark.parametrize("case", QKV_CASES)
 def test_qkv_project(case):
     qkv_check(case)
+
+
+# ---------------------------------------------------------------------------------------
+# together, and around them: graphs, streams, offsets past 32 bits, the status word
+# ---------------------------------------------------------------------------------------
+def shot(N_text, frames, rows, cols, seed):
+    """A packed shot of text and video with its metadata, positions and workload."""
+    import workloads as W
+    tokens = rows * cols
+    w = W.custom("layer%d" % seed, B=1, H=3, D=128, dtype="bf16", segments=[
+        W.Segment(W.TEXT, 1, N_text), W.Segment(W.PICTURE, 1, 48, pic=1),
+        W.Segment(W.TARGET, frames, tokens, frame_dt_s=4 / 24, mask=W.uniform_mask(seed, tokens)),
+        W.Segment(W.GUIDE, frames, tokens, frame_dt_s=4 / 24)],
+        params=W.Params(gain=(1.25,) + (1.0,) * 8), seed_index=700 + seed)
+    video = dict(frame_step=(4 / 24, 0, 0))
+    pos = T.pack_token_positions([
+        T.TokenGrid(N_text), T.TokenGrid(1, 6, 8, origin=(N_text, 0, 0)),
+        T.TokenGrid(frames, rows, cols, origin=(N_text + 1, 0, 0), **video),
+        T.TokenGrid(frames, rows, cols, origin=(N_text + 1, 0, 0), **video)])
+    assert len(pos) == w.N
+    return w, torch.from_numpy(pos).cuda()
+
+
+class Layer:
+    """One joint attention layer: text and the rest of the sequence have their own projections,
+    write rows of one packed q, k, v, attend jointly and return through their own output
+    projections with a gated residual."""
+
+    def __init__(self, w, pos, seed):
+        self.w, H, D = w, w.H, w.D
+        self.n_text = w.segments[0].length
+        self.C = H * D
+        self.x = rand((1, w.N, self.C), "bf16", seed)
+        self.part = []
+        for i in range(2):
+            self.part.append(dict(
+                w_qkv=rand((3 * self.C, self.C), "bf16", seed + 10 + i, self.C ** -0.5),
+                b_qkv=rand((3 * self.C,), "bf16", seed + 20 + i, 0.2),
+                wq=rand((D,), "bf16", seed + 30 + i, 0.1, 1.0),
+                wk=rand((D,), "bf16", seed + 40 + i, 0.1, 1.0),
+                w_out=rand((self.C, self.C), "bf16", seed + 50 + i, self.C ** -0.5),
+                b_out=rand((self.C,), "bf16", seed + 60 + i, 0.2),
+                gate=rand((1, self.C), "bf16", seed + 70 + i, 0.3, 0.5)))
+        self.meta = T.DeviceMeta(T.pack_token_meta(w.segments), "cuda")
+        self.table = T.rope_table(pos, (16, 56, 56))
+        self.qkv = [torch.empty((1, H, w.N, D), dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+        self.o, self.lse = torch.empty_like(self.qkv[0]), None
+        self.lse = torch.empty((1, H, w.N), dtype=torch.float32, device="cuda")
+        self.y = torch.empty_like(self.x)
+
+    def rows(self, i):
+        return slice(0, self.n_text) if i == 0 else slice(self.n_text, self.w.N)
+
+    def run(self):
+        for i, p in enumerate(self.part):
+            r = self.rows(i)
+            T.qkv_project(self.x[:, r], p["w_qkv"], self.w.H, bias=p["b_qkv"], q_weight=p["wq"],
+                          k_weight=p["wk"], table=self.table[r],
+                          out=[t[:, :, r] for t in self.qkv])
+        T.attn_forward(*self.qkv, self.meta, T.params_from(self.w.params), out=self.o, lse=self.lse)
+        for i, p in enumerate(self.part):
+            r = self.rows(i)
+            T.linear(self.o[:, :, r], p["w_out"], bias=p["b_out"], gate=p["gate"],
+                     residual=self.x[:, r], out=self.y[:, r])
+        return self.y
+
+
+@pytest.mark.parametrize("n_text", [40, 300])
+def test_a_layer_of_them(n_text):
+    from parity_util import compare, run_oracle
+    import oracle
+    w, pos = shot(n_text, 4, 7, 9, n_text)
+    layer = Layer(w, pos, n_text)
+    y = layer.run().clone()
+    assert T.device_status() == 0
+    a = ref.angles(pos.cpu().numpy(), (16, 56, 56), (1e4,) * 3)
+    assert np.abs(np64(layer.table) - np.stack([np.cos(a), np.sin(a)], -1)).max() < 4e-7
+    H, D = w.H, w.D
+    for i, p in enumerate(layer.part):
+        r = layer.rows(i)
+        x64 = np64(layer.x[0, r])
+        v, e = ref.product(x64, np64(p["w_qkv"]), np64(p["b_qkv"]))
+        v, e = (t.reshape(len(x64), 3, H, D).transpose(1, 2, 0, 3) for t in (v, e))
+        for j, key in enumerate(("wq", "wk", None)):
+            value, bound = (v[j], e[j]) if key is None else ref.norm_rope(
+                v[j], np64(p[key]), float(np.float32(1e-6)), True, np64(layer.table[r]), False, e[j])
+            close(layer.qkv[j][0, :, r], value, bound, "bf16")
+        # the output projection of what the attention returned
+        o64 = np64(layer.o[0, :, r]).transpose(1, 0, 2).reshape(len(x64), -1)
+        value, bound = ref.linear(o64, np64(p["w_out"]), np64(p["b_out"]), "none", np64(p["gate"]),
+                                  x64)
+        close(y[0, r], value, bound, "bf16")
+    rows = oracle.all_rows(1, H, w.N)
+    compare(w, layer.o, layer.lse, rows, *run_oracle(w, *layer.qkv, rows), "bf16")
+
+
+def test_a_captured_layer_replays_on_new_inputs():
+    w, pos = shot(40, 3, 6, 8, 3)
+    layer = Layer(w, pos, 5)
+    want = [layer.run().clone()]                      # also sizes the attention's workspace
+    first = layer.x.clone()
+    second = rand(tuple(first.shape), "bf16", 99)
+    layer.x.copy_(second)
+    want.append(layer.run().clone())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.run()
+    for x, y in zip((first, second, first), (want[0], want[1], want[0])):
+        layer.x.copy_(x)
+        layer.y.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(layer.y, y)
+
+
+@pytest.mark.parametrize("N", [3, 200, 700])
+def test_streams_side_by_side(N):
+    # calls on two streams at once, outputs allocated on theirs, give what one stream gives
+    x, w, o = linear_inputs(1, N, 512, 768, "bf16", 4, "bgr")
+    want = T.linear(x, w, act="silu", **o)
+    q = rand((1, 4, N, 128), "bf16", 8)
+    table = table_for(N, (64,), 9)
+    want_q = T.qk_norm_rope(q, table=table)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(4):
+        for s in streams:
+            got.append((T.linear(x, w, act="silu", stream=s, **o),
+                        T.qk_norm_rope(q, table=table, stream=s)))
+    for s in streams:
+        s.synchronize()
+    for y, z in got:
+        assert torch.equal(y, want) and torch.equal(z, want_q)
+
+
+def test_offsets_past_32_bits():
+    # more than 2^31 elements: an output of the linear layer, then the norm in place
+    N, K, C = 70001, 64, 32768
+    x, w, _ = linear_inputs(1, N, K, C, "bf16", 0, "")
+    y = T.linear(x, w)
+    assert y.numel() > 2 ** 31
+    rows = torch.tensor([0, 65535, 65536, 65537, 69887, 70000], device="cuda")
+    value, bound = ref.linear(np64(x[0, rows]), np64(w))
+    close(y[0, rows], value, bound, "bf16")
+    heads = y.view(1, N, 256, 128).transpose(1, 2)
+    before = heads[:, :, rows].clone()
+    T.qk_norm_rope(heads, q_out=heads)
+    value, bound = ref.norm_rope(np64(before), 1.0, float(np.float32(1e-6)), True, None, False)
+    close(heads[:, :, rows], value, bound, "bf16")
+
+
+@pytest.mark.parametrize("N", [4, 300])
+def test_launches_skip_while_the_status_word_is_set(N):
+    x, w, _ = linear_inputs(1, N, 256, 512, "bf16", 0, "")
+    y = torch.full((1, N, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    assert T.device_status() == 0
+    T.selftest_wait(5000, arrive=False)
+    T.linear(x, w, out=y)
+    assert T.device_status() == -10
+    assert bool((y == 3.0).all())
+    value, bound = ref.linear(np64(x[0]), np64(w))
+    close(T.linear(x, w, out=y), value, bound, "bf16")
+
+
+def test_the_binding_refuses():
+    x, w, o = linear_inputs(1, 6, 64, 128, "bf16", 0, "bgr")
+    bad = [
+        lambda: T.linear(x, w.t()), lambda: T.linear(x, w[:, :32]), lambda: T.linear(x, w.float()),
+        lambda: T.linear(x, w, bias=o["bias"][:64]), lambda: T.linear(x, w, act="relu"),
+        lambda: T.linear(x, w, bias=o["bias"].float()), lambda: T.linear(x, w, heads=3),
+        lambda: T.linear(x.transpose(1, 2), w), lambda: T.linear(x[None, None], w),
+        lambda: T.linear(x, w, out=torch.empty(1, 6, 64, dtype=x.dtype, device="cuda")),
+        lambda: T.linear(x, w.cpu()), lambda: T.qkv_project(x, w, 3),
+        lambda: T.qkv_project(x, w[:96], 1, norm=False, q_weight=o["bias"][:32]),
+        lambda: T.qk_norm_rope(x), lambda: T.qk_norm_rope(x[None], table=table_for(5, (64,), 1)),
+        lambda: T.qk_norm_rope(x[None], k_out=x[None]),
+        lambda: T.qk_norm_rope(x[None], norm=False, q_weight=o["bias"][:64]),
+        lambda: T.qk_norm_rope(x[None], pairing="thirds", table=table_for(6, (64,), 1)),
+        lambda: T.rope_table(x[0].float(), (64,)), lambda: T.rope_table(x[0], (64,)),
+    ]
+    for f in bad:
+        with pytest.raises((ValueError, TypeError)):
+            f()
+    for f in (lambda: T.qk_norm_rope(x[None], norm=False), lambda: T.linear(x[:, :1].expand(1, 6, 64), w),
+              lambda: T.linear(x, w, out=x)):
+        with pytest.raises((T.TaraError, ValueError)):
+            f()
+    torch.cuda.synchronize()

@@ -197,6 +197,8 @@ def test_linear_refuses_null(lib):
     (stream_view(FAKE + 2, 300, 256), ALIGN),
     (view(FAKE, shape=(1, 1, 300, 256), strides=(0, 0, 260)), ALIGN),
     (stream_view(FAKE3, 300, 256), PARAM),                             # y over x
+    (view(FAKE, shape=(1, 1, 300, 256), strides=(0, 0, 0)), PARAM),    # one row, expanded
+    (view(FAKE, shape=(1, 2, 300, 128), strides=(0, 0, 128)), PARAM),  # one head, expanded
 ])
 def test_linear_refuses_inputs(lib, x, want):
     assert call_linear(lib, x=x) == want

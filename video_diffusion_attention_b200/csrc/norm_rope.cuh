@@ -167,13 +167,14 @@ __device__ __forceinline__ float2 turn_quarters(float2 sc, int q) {
 }
 
 // Write-bound (8 bytes a pair).  A thread keeps two neighbouring pairs (one 16-byte store) and
-// walks rows with the stride of the grid, kRopeBatch rows' positions in flight, so that pair
+// walks rows with the stride of the grid, the next kRopeBatch positions in flight, so that pair
 // index, axis and frequency are set up once.  The frequencies pass through shared memory: read
 // by thread index from the kernel's arguments they are fetched one address at a time, which with
 // 8 rows a thread took half of the time.
 constexpr int kRopeBatch = 4;
+constexpr int kRopeCtas = 5;      // CTAs that run together on an SM
 
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
 rope_table_kernel(const float* __restrict__ pos, long long n_rows,
                   const __grid_constant__ RopeFreqs fr, float4* __restrict__ table) {
   __shared__ double s_freq[kRopeMaxPairs];
@@ -192,27 +193,39 @@ rope_table_kernel(const float* __restrict__ pos, long long n_rows,
   const float* p1 = pos + s_axis[2 * u + 1];
   const int n_axes = fr.n_axes;
   const long long stride = (long long)gridDim.x * rows_step;
-  for (long long row0 = (long long)blockIdx.x * rows_step + r; row0 < n_rows;
-       row0 += kRopeBatch * stride) {
-    float x[kRopeBatch], y[kRopeBatch];
+  float x[kRopeBatch], y[kRopeBatch];
+  auto fetch = [&](long long row0) {
 #pragma unroll
     for (int i = 0; i < kRopeBatch; ++i) {
       const long long row = min(row0 + i * stride, n_rows - 1);
       x[i] = __ldg(p0 + row * n_axes);
       y[i] = __ldg(p1 + row * n_axes);
     }
+  };
+  long long row0 = (long long)blockIdx.x * rows_step + r;
+  fetch(row0);
+  while (row0 < n_rows) {
+    float nx[kRopeBatch], ny[kRopeBatch];
+#pragma unroll
+    for (int i = 0; i < kRopeBatch; ++i) {
+      nx[i] = x[i];
+      ny[i] = y[i];
+    }
+    const long long next = row0 + kRopeBatch * stride;
+    if (next < n_rows) fetch(next);
 #pragma unroll
     for (int i = 0; i < kRopeBatch; ++i) {
       const long long row = row0 + i * stride;
       if (row >= n_rows) break;
       int q0, q1;
-      const float a0 = quarter_turn_remainder((double)x[i], f0, q0);
-      const float a1 = quarter_turn_remainder((double)y[i], f1, q1);
+      const float a0 = quarter_turn_remainder((double)nx[i], f0, q0);
+      const float a1 = quarter_turn_remainder((double)ny[i], f1, q1);
       float2 sc[2];
       sin_cos_small2(a0, a1, sc);
       const float2 t0 = turn_quarters(sc[0], q0), t1 = turn_quarters(sc[1], q1);
       table[row * row_units + u] = make_float4(t0.x, t0.y, t1.x, t1.y);
     }
+    row0 = next;
   }
 }
 

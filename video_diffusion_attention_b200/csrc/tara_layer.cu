@@ -88,15 +88,18 @@ RowView row_view(const tara_view& v) {
   return RowView{n.ptr, n.stride_b, n.stride_h, n.stride_n, n.D};
 }
 
-// A view of the linear layer: 16-bit views are read and written by 16-byte chunks and 64-column
-// boxes of the tensor maps; the fp32 kernel takes anything.
-int check_linear_view(const tara_view* v, bool out) {
+// A view of the linear layer: 16-bit views are read and written by 16-byte chunks, x by 64-column
+// boxes of a tensor map (whose strides may not be 0); the fp32 kernels take anything.
+int check_linear_view(const tara_view* v, bool out, bool mapped) {
   if (!v) return TARA_ERR_NULL;
   const int align = v->dtype == TARA_FP32 ? 0 : 16;
   const int rc = out ? check_out_view(v, align) : check_view(v, align);
   if (rc != TARA_OK) return rc;
-  if (v->dtype != TARA_FP32 && (v->D % 8 != 0 || (v->H > 1 && v->D % 64 != 0)))
-    return TARA_ERR_SHAPE;
+  if (v->dtype == TARA_FP32) return TARA_OK;
+  if (v->D % 8 != 0 || (v->H > 1 && v->D % 64 != 0)) return TARA_ERR_SHAPE;
+  if (mapped && ((v->B > 1 && v->stride_b == 0) || (v->H > 1 && v->stride_h == 0) ||
+                 (v->N > 1 && v->stride_n == 0)))
+    return TARA_ERR_PARAM;
   return TARA_OK;
 }
 
@@ -386,9 +389,9 @@ int tara_rope_table(const float* pos, int64_t n_rows, const tara_rope* rope, flo
       fr.quarter_turns[fr.n_pairs++] =
           std::pow(rope->theta[a], -2.0 * i / rope->dim[a]) * 0.63661977236758134308;   // 2/pi
     }
-  // one row a thread, up to the CTAs that run together (6 an SM)
+  // one row a thread, up to the CTAs that run together
   const long long rows_step = kRopeThreads / (fr.n_pairs / 2);
-  const long long grid = std::min<long long>((n_rows - 1) / rows_step + 1, 148 * 6);
+  const long long grid = std::min<long long>((n_rows - 1) / rows_step + 1, 148 * kRopeCtas);
   if (n_rows > ((int64_t)1 << 40)) return TARA_ERR_TOO_LARGE;
   rope_table_kernel<<<(unsigned)grid, kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(
       pos, n_rows, fr, reinterpret_cast<float4*>(table));
@@ -426,7 +429,7 @@ int tara_linear(const tara_view* x, const void* w, const tara_epilogue* e, tara_
                 void* stream) {
   if (!x || !w || !y) return TARA_ERR_NULL;
   int rc;
-  if ((rc = check_linear_view(x, false)) != TARA_OK || (rc = check_linear_view(y, true)) != TARA_OK)
+  if ((rc = check_linear_view(x, false, true)) != TARA_OK || (rc = check_linear_view(y, true, false)) != TARA_OK)
     return rc;
   if (x->dtype != y->dtype) return TARA_ERR_DTYPE;
   if (x->B != y->B || x->N != y->N) return TARA_ERR_SHAPE;
@@ -453,7 +456,7 @@ int tara_linear(const tara_view* x, const void* w, const tara_epilogue* e, tara_
     a.gate_b = e->gate_stride;
     if (e->residual) {
       const tara_view* r = e->residual;
-      if ((rc = check_linear_view(r, false)) != TARA_OK) return rc;
+      if ((rc = check_linear_view(r, false, false)) != TARA_OK) return rc;
       if (r->dtype != x->dtype) return TARA_ERR_DTYPE;
       if (r->B != y->B || r->N != y->N || columns(*r) != columns(*y)) return TARA_ERR_SHAPE;
       if (r->ptr == y->ptr && !same_layout(*r, *y)) return TARA_ERR_PARAM;
@@ -468,7 +471,7 @@ int tara_qkv_project(const tara_view* x, const void* w, const void* bias,
                      void* stream) {
   if (!x || !w || !q || !k || !v) return TARA_ERR_NULL;
   int rc;
-  if ((rc = check_linear_view(x, false)) != TARA_OK) return rc;
+  if ((rc = check_linear_view(x, false, true)) != TARA_OK) return rc;
   const tara_view* outs[3] = {q, k, v};
   for (const tara_view* o : outs) {
     if ((rc = check_out_view(o, 16)) != TARA_OK) return rc;
