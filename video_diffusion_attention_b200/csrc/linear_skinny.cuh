@@ -4,7 +4,8 @@
 // tensor rate of the measured ridge).  So the roles are swapped: 128 rows of W are the M = 128
 // operand of tcgen05.mma, kT tokens (16 to 128) the N operand, and no lane of the tensor core
 // multiplies padding when there is one token.  K is split over the CTAs of a cluster, so that C/128
-// tiles still fill the device; each keeps a ring of 16 KB weight tiles in flight (two CTAs an SM).
+// tiles still fill the device; each keeps a ring of 16 KB weight tiles in flight (up to three CTAs an
+// SM, so that one streams while another starts or ends).
 // The partial sums meet in the CTAs' shared memory: CTA r of a cluster of S takes tokens r, r + S,
 // ..., reads the S partials of each through distributed shared memory in rank order (the same
 // bits every time, no atomics, no workspace that two captured graphs could share) and finishes
@@ -23,8 +24,8 @@ struct SkinnyLin {
   static constexpr int kWBytes = 128 * 128;
   static constexpr int kXBytes = kT * 128;
   static constexpr int kStageBytes = kWBytes + kXBytes;
-  static constexpr int kCtas = kT <= 128 ? 2 : 1;                // an SM
-  static constexpr int kStages = 196608 / kCtas / kStageBytes;   // 5 (16 tokens) to 3 (128); 4
+  static constexpr int kCtas = kT <= 64 ? 3 : (kT == 128 ? 2 : 1);        // an SM
+  static constexpr int kStages = (kCtas == 3 ? 73728 : 196608 / kCtas) / kStageBytes;   // 3 or 4
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + (2 * kStages + 1) * 8 + 16;
   static constexpr uint32_t kTmemCols = kT < 32 ? 32 : kT;
   static_assert(kT * 128 * 4 <= kStages * kStageBytes, "the partial sums reuse the ring");
