@@ -278,21 +278,33 @@ __device__ __forceinline__ void pair_heads_ahead(const LinearArgs& a, const Head
   }
 }
 
-// 8 accumulators from column d of a head: bias, norm (r: its factor) and weight.
+// Bias and norm weight of 8 columns of a head, loaded before the accumulators are waited for.
+struct PairParams8 {
+  uint4 bias, weight;
+};
+__device__ __forceinline__ PairParams8 pair_params8(const uint16_t* bias, const uint16_t* weight,
+                                                    int d) {
+  PairParams8 p;
+  p.bias = bias ? ldg16(bias, d) : make_uint4(0u, 0u, 0u, 0u);
+  p.weight = weight ? ldg16(weight, d) : make_uint4(0u, 0u, 0u, 0u);
+  return p;
+}
+
+// 8 accumulators: bias, norm (r: its factor) and weight.
 template <bool kBF16>
-__device__ __forceinline__ void pair_finish8(const uint32_t* v, const uint16_t* bias,
-                                             const uint16_t* weight, int d, float r, float* f) {
+__device__ __forceinline__ void pair_finish8(const uint32_t* v, const PairParams8& p, bool bias,
+                                             bool weight, float r, float* f) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(v[j]);
   if (bias) {
     float t[8];
-    unpack8<kBF16>(ldg16(bias, d), t);
+    unpack8<kBF16>(p.bias, t);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] += t[j];
   }
   if (weight) {
     float t[8];
-    unpack8<kBF16>(ldg16(weight, d), t);
+    unpack8<kBF16>(p.weight, t);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] *= r * t[j];
   } else {
@@ -390,6 +402,8 @@ __device__ __forceinline__ void pair_heads(const LinearArgs& a, const PairWarp& 
           uint32_t v[16];
           tmem_ld8(acc + d, v);
           tmem_ld8(acc + d + half, v + 8);
+          const PairParams8 lo = pair_params8(bias, weight, d);
+          const PairParams8 hi = pair_params8(bias, weight, d + half);
           float t[16];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -402,8 +416,8 @@ __device__ __forceinline__ void pair_heads(const LinearArgs& a, const PairWarp& 
           tmem_ld_wait();
           reg_fence<16>(v);
           float f[16];
-          pair_finish8<kBF16>(v, bias, weight, d, r, f);
-          pair_finish8<kBF16>(v + 8, bias, weight, d + half, r, f + 8);
+          pair_finish8<kBF16>(v, lo, bias != nullptr, weight != nullptr, r, f);
+          pair_finish8<kBF16>(v + 8, hi, bias != nullptr, weight != nullptr, r, f + 8);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float x = f[j], z = f[j + 8], c = t[2 * j], s = t[2 * j + 1];
@@ -415,16 +429,19 @@ __device__ __forceinline__ void pair_heads(const LinearArgs& a, const PairWarp& 
         }
       } else {
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 4; q += 2) {
           const int d = first + q * 8;
           if (d >= last) break;
-          uint32_t v[8];
+          const bool two = d + 8 < last;                 // only behind R can a block be alone
+          uint32_t v[16];
           tmem_ld8(acc + d, v);
-          float t[8];
-          const bool turns = turned && d < ah.rot;
-          if (turns) {
+          tmem_ld8(acc + (two ? d + 8 : d), v + 8);
+          const PairParams8 lo = pair_params8(bias, weight, d);
+          const PairParams8 hi = pair_params8(bias, weight, two ? d + 8 : d);
+          float t[16];
+          if (turned) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 4; ++j) {
               const uint4 c4 = ld_shared_v4(stage128(w.buf, w.lane, 2 * q + j));
               t[4 * j] = __uint_as_float(c4.x);
               t[4 * j + 1] = __uint_as_float(c4.y);
@@ -433,18 +450,22 @@ __device__ __forceinline__ void pair_heads(const LinearArgs& a, const PairWarp& 
             }
           }
           tmem_ld_wait();
-          reg_fence<8>(v);
-          float f[8];
-          pair_finish8<kBF16>(v, bias, weight, d, r, f);
-          if (turns) {
+          reg_fence<16>(v);
+          float f[16];
+          pair_finish8<kBF16>(v, lo, bias != nullptr, weight != nullptr, r, f);
+          pair_finish8<kBF16>(v + 8, hi, bias != nullptr, weight != nullptr, r, f + 8);
+          if (turned) {
+            // R is a multiple of 8: a block turns as a whole or not at all
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 8; ++j) {
+              if (d + (j & 4 ? 8 : 0) >= ah.rot) break;
               const float x = f[2 * j], z = f[2 * j + 1], c = t[2 * j], s = t[2 * j + 1];
               f[2 * j] = fmaf(x, c, -z * s);
               f[2 * j + 1] = fmaf(x, s, z * c);
             }
           }
           pair_stage8<kBF16>(stage128(w.buf, w.lane, 2 * q), f);
+          pair_stage8<kBF16>(stage128(w.buf, w.lane, 2 * q + 2), f + 8);
         }
       }
       __syncwarp();
