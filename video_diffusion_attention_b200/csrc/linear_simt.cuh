@@ -20,7 +20,7 @@ constexpr int kSimtLinThreads = 256;
 // The activations once more for single fp32 results, by CUDA's own functions.
 __device__ __forceinline__ float simt_activate(float v, int act) {
   if (act == 1) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-  if (act == 2) return v / (1.0f + expf(-1.59576912160573072f * (v + 0.044715f * v * v * v)));
+  if (act == 2) return v / (1.0f + expf(-1.5957691216f * (v + 0.044715f * v * v * v)));
   if (act == 3) return v / (1.0f + expf(-v));
   return v;
 }
