@@ -267,7 +267,7 @@ int tara_device_status(void* stream);
 
 /* Debug build.  The library can be compiled with -DTARA_DEBUG=1 (python -m
  * video_diffusion_attention_b200.build --debug writes libtara_attn_debug.so beside the release
- * library).  Its kernels then check on the device what the host cannot see: that target and
+ * library).  The attention kernels then check on the device what the host cannot see: that target and
  * guide tokens carry finite times and target tokens finite mask weights, and that every row,
  * plane and output index they derive stays inside its array.  A failed check records itself
  * in the status word, the checked access is skipped and nothing traps; tara_device_status
