@@ -87,6 +87,12 @@ def _view(t) -> TaraView:
     return TaraView(t.data_ptr(), _dtype(t), 1, 1, shape[0], shape[1], 0, 0, stride[0])
 
 
+def _new(like, B, H, N, D):
+    """A new contiguous [B][H][N][D] tensor like `like`, and its view."""
+    t = like.new_empty((B, H, N, D))
+    return t, TaraView(t.data_ptr(), _dtype(like), B, H, N, D, H * N * D, N * D, D)
+
+
 def _vector(t, name: str, like, *shapes) -> Optional[int]:
     """Pointer of an optional contiguous parameter of one of the given shapes."""
     if t is None:
@@ -218,15 +224,14 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, eps: float = 1e-6, nor
         raise ValueError("k_out and k_weight need k")
     B, H, N, D = q.shape
     p = _norm_rope_struct(q, H, N, D, B, q_weight, k_weight, eps, norm, table, pairing)
-    if q_out is None:
-        q_out = q.new_empty((B, H, N, D))
+    qv = _view(q)
+    q_out, qo = _new(q, B, H, N, D) if q_out is None else (q_out, _view(q_out))
     kv = ko = None
     if k is not None:
-        if k_out is None:
-            k_out = q.new_empty((B, H, N, D))
-        kv, ko = ctypes.byref(_view(k)), ctypes.byref(_view(k_out))
-    _check(load_library().tara_qk_norm_rope(ctypes.byref(_view(q)), kv, ctypes.byref(p),
-                                            ctypes.byref(_view(q_out)), ko, _current_stream(q)),
+        k_out, ko = _new(q, B, H, N, D) if k_out is None else (k_out, _view(k_out))
+        kv, ko = ctypes.byref(_view(k)), ctypes.byref(ko)
+    _check(load_library().tara_qk_norm_rope(ctypes.byref(qv), kv, ctypes.byref(p),
+                                            ctypes.byref(qo), ko, _current_stream(q)),
            "tara_qk_norm_rope")
     return q_out if k is None else (q_out, k_out)
 
@@ -301,11 +306,12 @@ def qkv_project(x, w, heads: int, bias=None, q_weight=None, k_weight=None, eps: 
         raise ValueError("weights are only used with the norm")
     bias_ptr = _vector(bias, "bias", x, (rows,))
     if out is None:
-        shape = (B, heads, N, D)
-        out = (x.new_empty(shape), x.new_empty(shape), x.new_empty(shape))
-    q, k, v = out
-    _same_device(x, q, k, v)
+        (q, qv), (k, kv), (v, vv) = (_new(x, B, heads, N, D) for _ in range(3))
+    else:
+        q, k, v = out
+        _same_device(x, q, k, v)
+        qv, kv, vv = _view(q), _view(k), _view(v)
     _check(load_library().tara_qkv_project(
-        ctypes.byref(xv), w.data_ptr(), bias_ptr, p, ctypes.byref(_view(q)),
-        ctypes.byref(_view(k)), ctypes.byref(_view(v)), _current_stream(x)), "tara_qkv_project")
+        ctypes.byref(xv), w.data_ptr(), bias_ptr, p, ctypes.byref(qv), ctypes.byref(kv),
+        ctypes.byref(vv), _current_stream(x)), "tara_qkv_project")
     return q, k, v

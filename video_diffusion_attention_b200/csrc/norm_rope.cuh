@@ -189,43 +189,46 @@ rope_table_kernel(const float* __restrict__ pos, long long n_rows,
   const int r = threadIdx.x / row_units, u = threadIdx.x - r * row_units;
   if (r >= rows_step) return;
   const double f0 = s_freq[2 * u], f1 = s_freq[2 * u + 1];
-  const float* p0 = pos + s_axis[2 * u];
-  const float* p1 = pos + s_axis[2 * u + 1];
-  const int n_axes = fr.n_axes;
   const long long stride = (long long)gridDim.x * rows_step;
+  const long long row0 = (long long)blockIdx.x * rows_step + r;
+  // pointers and a count of the rows ahead instead of 64-bit row numbers in the loop
+  const long long pos_step = stride * fr.n_axes, out_step = stride * row_units;
+  const float* p0 = pos + row0 * fr.n_axes + s_axis[2 * u];
+  const int to1 = (int)s_axis[2 * u + 1] - (int)s_axis[2 * u];
+  float4* out = table + row0 * row_units + u;
+  long long left = row0 < n_rows ? (n_rows - row0 + stride - 1) / stride : 0;
   float x[kRopeBatch], y[kRopeBatch];
-  auto fetch = [&](long long row0) {
+  auto fetch = [&](long long rows) {
 #pragma unroll
     for (int i = 0; i < kRopeBatch; ++i) {
-      const long long row = min(row0 + i * stride, n_rows - 1);
-      x[i] = __ldg(p0 + row * n_axes);
-      y[i] = __ldg(p1 + row * n_axes);
+      if (i < rows) {
+        x[i] = __ldg(p0);
+        y[i] = __ldg(p0 + to1);
+      }
+      p0 += pos_step;
     }
   };
-  long long row0 = (long long)blockIdx.x * rows_step + r;
-  fetch(row0);
-  while (row0 < n_rows) {
+  fetch(left);
+  for (; left > 0; left -= kRopeBatch) {
     float nx[kRopeBatch], ny[kRopeBatch];
 #pragma unroll
     for (int i = 0; i < kRopeBatch; ++i) {
       nx[i] = x[i];
       ny[i] = y[i];
     }
-    const long long next = row0 + kRopeBatch * stride;
-    if (next < n_rows) fetch(next);
+    fetch(left - kRopeBatch);
 #pragma unroll
     for (int i = 0; i < kRopeBatch; ++i) {
-      const long long row = row0 + i * stride;
-      if (row >= n_rows) break;
+      if (i >= left) break;
       int q0, q1;
       const float a0 = quarter_turn_remainder((double)nx[i], f0, q0);
       const float a1 = quarter_turn_remainder((double)ny[i], f1, q1);
       float2 sc[2];
       sin_cos_small2(a0, a1, sc);
       const float2 t0 = turn_quarters(sc[0], q0), t1 = turn_quarters(sc[1], q1);
-      table[row * row_units + u] = make_float4(t0.x, t0.y, t1.x, t1.y);
+      *out = make_float4(t0.x, t0.y, t1.x, t1.y);
+      out += out_step;
     }
-    row0 = next;
   }
 }
 
