@@ -219,6 +219,9 @@ LINEAR_CASES = [
     (2, 257, 256, 512, "bf16", 2, "bgr", None, None),
     (1, 300, 104, 776, "fp16", 0, "bg", "gelu", None),
     (1, 513, 640, 264, "bf16", 0, "", "gelu_tanh", None),
+    (1, 512, 192, 7168, "bf16", 0, "bgr", "silu", None),     # 208 columns a tile
+    (1, 560, 136, 7176, "fp16", 0, "bgr", None, None),       # 160, and a ragged end
+    (2, 520, 128, 4600, "bf16", 2, "br", "gelu", None),
     (1, 1000, 512, 1536, "bf16", 4, "bgr", None, None),
     (2, 700, 328, 520, "fp16", 0, "br", "silu", None),
     (1, 2100, 256, 2304, "bf16", 0, "b", None, 18),

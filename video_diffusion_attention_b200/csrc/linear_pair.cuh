@@ -73,6 +73,8 @@ struct PairLinArgs {
   LinearArgs lin;
   HeadArgs head;
   int m_tiles, n_tiles;    // row tiles of one branch, column tiles
+  int bn;                  // columns of a tile: BN, or less (a multiple of 16) where one head and
+                           // one part make up the output's row
   int group;               // row tiles walked together (L2 reuse of W)
 };
 
@@ -92,6 +94,7 @@ struct PairWarp {
   uint32_t buf;      // staging
   uint32_t release;  // shared::cluster address of the accumulator's acc_empty barrier
   int b, r0, c0, lane;
+  int c_end;         // the tile's columns end here
 };
 
 // The warp has read its part of the accumulator: the MMA warp may start the unit after next in it.
@@ -131,7 +134,7 @@ __device__ __forceinline__ void pair_load_residual(const PairLinearAhead& ah, in
 
 __device__ __forceinline__ void pair_linear_ahead(const LinearArgs& a, const PairWarp& w,
                                                   PairLinearAhead& ah) {
-  ah.cols = min(128, a.C - w.c0);
+  ah.cols = min(128, w.c_end - w.c0);
   ah.rows = min(32, a.N - w.r0);
   ah.bias = a.bias ? static_cast<const uint16_t*>(a.bias) + w.c0 : nullptr;
   ah.gate = a.gate ? static_cast<const uint16_t*>(a.gate) + w.b * a.gate_b + w.c0 : nullptr;
@@ -260,7 +263,7 @@ __device__ __forceinline__ void pair_heads_ahead(const LinearArgs& a, const Head
   ah.k_weight = static_cast<const uint16_t*>(head.weight[1]);
   ah.weight_h = head.weight_h;
   ah.bias = a.bias ? static_cast<const uint16_t*>(a.bias) + w.c0 : nullptr;
-  ah.cols = min(128, a.C - w.c0);
+  ah.cols = min(128, w.c_end - w.c0);
   ah.rows = min(32, a.N - w.r0);
   ah.D = head.D;
   ah.rot = head.rot;
@@ -526,7 +529,7 @@ linear_pair_kernel(const __grid_constant__ PairLinMaps maps,
     const int g = t / span, r = t - g * span;
     const int rows = min(args.group, rows_t - g * args.group);
     const int mt = g * args.group + r % rows;
-    c0 = (r / rows) * BN;
+    c0 = (r / rows) * args.bn;
     b = mt / args.m_tiles;
     m0 = (mt - b * args.m_tiles) * (256 * kSubs);
   };
@@ -582,10 +585,10 @@ linear_pair_kernel(const __grid_constant__ PairLinMaps maps,
         int b, m0, c0;
         decode(t, b, m0, c0);
         const int row = m0 + (int)rank * 128;
-        const int wrow = c0 + (int)rank * (BN / 2);
+        const int wrow = c0 + (int)rank * (args.bn / 2);
         // a second sub-tile wholly behind the last row is neither loaded nor multiplied
         const int subs = kSubs == 2 && m0 + 256 < a.N ? 2 : 1;
-        const uint32_t bytes = 2u * (uint32_t)(subs * 16384 + S::kBBytes);
+        const uint32_t bytes = 2u * (uint32_t)(subs * 16384 + args.bn * 64);
         int h = 0, d = 0;      // column of x: (head, column of the head)
         for (int k = 0; k < k_steps; ++k) {
           if (!(ok = mbar_wait_idle(&empty[slot], phase ^ 1u, abort_flag))) break;
@@ -613,7 +616,7 @@ linear_pair_kernel(const __grid_constant__ PairLinMaps maps,
       }
     } else if (warp == 1 && lane == 0 && leader) {
       // ------------------------------ MMA issuer (even CTA) ----------------------------
-      constexpr uint32_t idesc = make_idesc_f16(256, BN, kBF16, false);
+      const uint32_t idesc = make_idesc_f16(256, args.bn, kBF16, false);
       const uint64_t ad0 = make_sdesc_sw128(smem_u32(smem), 16, 1024);
       const uint64_t bd0 = make_sdesc_sw128(smem_u32(smem + S::kABytes), 16, 1024);
       bool ok = true;
@@ -699,6 +702,7 @@ linear_pair_kernel(const __grid_constant__ PairLinMaps maps,
     for (int t = first; ok && t < n_tiles_total; t += n_clusters) {
       int m0;
       decode(t, w.b, m0, w.c0);
+      w.c_end = min(a.C, w.c0 + args.bn);
       if (BN == 256) w.c0 += grp * 128;
 #pragma unroll 1
       for (int u = 0; u < kSubs; ++u, ++unit) {
@@ -706,7 +710,7 @@ linear_pair_kernel(const __grid_constant__ PairLinMaps maps,
         if (BN == 128 && half != (uint32_t)grp) continue;
         w.r0 = m0 + u * 256 + (int)rank * 128 + wq * 32;
         w.acc = tmem + lane_base + half * BN + (BN == 256 ? grp * 128 : 0);
-        const bool live = w.r0 < a.N && w.c0 < a.C;
+        const bool live = w.r0 < a.N && w.c0 < w.c_end;
         w.release = acc_empty_l + half * 8u;
         // the first piece of what comes from memory, in flight while the products run
         typename std::conditional<kQkv, PairHeadsAhead, PairLinearAhead>::type ahead;

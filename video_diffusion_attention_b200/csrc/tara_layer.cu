@@ -166,11 +166,11 @@ struct PairLauncher {
     PairLinArgs p = args;
     PairLinMaps maps;
     if ((rc = encode_view(dev, &maps.x, dt, a.x, a.B, a.N, a.K, 128)) != TARA_OK ||
-        (rc = encode_weights(dev, &maps.w, dt, a.w, a.C, a.K, BN / 2)) != TARA_OK)
+        (rc = encode_weights(dev, &maps.w, dt, a.w, a.C, a.K, p.bn / 2)) != TARA_OK)
       return rc;
     constexpr int rows = 256 * kSubs;
     p.m_tiles = (int)(((long long)a.N + rows - 1) / rows);
-    p.n_tiles = (int)(((long long)a.C + BN - 1) / BN);
+    p.n_tiles = (int)(((long long)a.C + p.bn - 1) / p.bn);
     p.group = 8 / kSubs;
     const long long tiles = (long long)a.B * p.m_tiles * p.n_tiles;
     const long long clusters = std::min<long long>(tiles, std::max(1, dev.sms / 2));
@@ -328,32 +328,41 @@ int run_linear(LinearArgs a, const HeadArgs* head, tara_dtype dt, cudaStream_t s
   PairLinArgs p{};
   p.lin = a;
   if (head) p.head = *head;
-  // Tile size by the estimated cycles of a cluster's rounds.  A 64-column K step takes 512 (256 x
-  // 256) or 1,024 cycles (512 x 256) of the tensor cores; 256 x 128 needs 256, but its 24 KB of
-  // operands an SM arrive at about 64 bytes a cycle, so 384.  What a round costs beyond its
-  // products (filling the ring, the last tile's epilogue) counts as 8 K steps.
+  // Tile width by the estimated cycles of a cluster's rounds.  A 64-column K step of a 256 x bn
+  // tile takes 2 * bn cycles of the tensor cores, and its (256 + bn) * 64 bytes an SM arrive at
+  // about 64 bytes a cycle, which is the larger up to 256 columns.  What a round costs beyond its
+  // products (filling the ring, the last tile's epilogue) counts as 8 K steps.  Widths between
+  // 128 and 256 are for rows of one head and one part, where a tile may end anywhere (512 x 7,168
+  // -> 7,168 on 74 SM pairs: 70 tiles of 208 columns, 42 us, instead of 56 of 256, 44 us).
   const int pairs = std::max(1, dev.sms / 2);
   const long long k_steps = ((long long)a.K + 63) / 64;
-  auto cycles = [&](int rows, int cols, long long step) {
-    const long long tiles = (long long)a.B * (((long long)a.N + rows - 1) / rows) *
-                            (((long long)a.C + cols - 1) / cols);
-    return (tiles + pairs - 1) / pairs * k_steps * step + 8 * step;
-  };
-  const long long c256 = cycles(256, 256, 512), c128 = cycles(256, 128, 384);
-  int size = c128 < c256 ? 0 : 1;
+  const long long m_tiles = (long long)a.B * (((long long)a.N + 255) / 256);
+  const bool any_width = !heads && a.part_cols == a.C && a.y[0].D == a.C &&
+                         (!a.residual.ptr || a.residual.D == a.C);
+  long long best = 0;
+  for (int bn = 256; bn >= 128; bn -= any_width ? 16 : 128) {
+    const long long tiles = m_tiles * (((long long)a.C + bn - 1) / bn);
+    const long long cost = (tiles + pairs - 1) / pairs * k_steps * (256 + bn) + 8 * (256 + bn);
+    if (best == 0 || cost < best) {
+      best = cost;
+      p.bn = bn;
+    }
+  }
   // 512 x 256 reads a quarter less through L2 than 256 x 256, but its accumulators fill tensor
   // memory, so part of every epilogue is exposed (about 7,000 cycles).  Long calls run at the
   // power cap, where the saved traffic counts for more: 107,126 x 7,168 -> 7,168 back to back
   // takes 8.7 ms against 9.3; with 1,024 input columns the exposed epilogue loses (1.05 against
   // 0.69 ms).
-  if (size == 1 && k_steps >= 64 && tiles128 / 2 >= 32LL * pairs) size = 2;
+  const bool tall = k_steps >= 64 && tiles128 / 2 >= 32LL * pairs;
+  if (tall) p.bn = 256;
+  const bool narrow = p.bn == 128;
   if (dt == TARA_BF16) {
-    if (size == 2) return launch_pair<true, 256, 2>(dev, p, heads, dt, stream);
-    if (size == 1) return launch_pair<true, 256, 1>(dev, p, heads, dt, stream);
+    if (tall) return launch_pair<true, 256, 2>(dev, p, heads, dt, stream);
+    if (!narrow) return launch_pair<true, 256, 1>(dev, p, heads, dt, stream);
     return launch_pair<true, 128, 1>(dev, p, heads, dt, stream);
   }
-  if (size == 2) return launch_pair<false, 256, 2>(dev, p, heads, dt, stream);
-  if (size == 1) return launch_pair<false, 256, 1>(dev, p, heads, dt, stream);
+  if (tall) return launch_pair<false, 256, 2>(dev, p, heads, dt, stream);
+  if (!narrow) return launch_pair<false, 256, 1>(dev, p, heads, dt, stream);
   return launch_pair<false, 128, 1>(dev, p, heads, dt, stream);
 }
 
