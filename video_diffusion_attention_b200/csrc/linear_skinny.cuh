@@ -72,57 +72,96 @@ __device__ __forceinline__ float4 load4(const void* p, long long i) {
   return make_float4(lo.x, lo.y, hi.x, hi.y);
 }
 
-// One token's 4 columns from column c of the output (all lanes of the warp together cover 128
-// columns): bias, then act/gate/residual or the head's norm and rotation, then the store.
+// What one lane needs to finish its 4 columns of any token (all lanes of a warp together cover the
+// CTA's 128 columns): parameters in registers, addresses as base and strides.  Gathered while the
+// products run; computed per token it made each take 800 cycles.
+struct SkinnyLane {
+  bool ok;                  // the columns exist
+  int part, l, d;           // output part; lane and column within the head (projection)
+  float4 bias, gain;        // gain: gate (when shared by the branches) or norm weight
+  uint16_t* y;
+  const uint16_t* residual;
+  const uint16_t* gate;     // per branch
+  long long y_b, y_n, r_b, r_n, gate_b;
+};
+
 template <bool kBF16, bool kQkv>
-__device__ __forceinline__ void skinny_finish(const LinearArgs& a, const HeadArgs& head, float4 s,
-                                              int b, int n, int c) {
-  const bool ok = c < a.C;
-  const int part = ok ? c / a.part_cols : 0;
-  const int pc = ok ? c - part * a.part_cols : 0;
-  float f[4] = {s.x, s.y, s.z, s.w};
-  if (a.bias && ok) {
-    const float4 t = load4<kBF16>(a.bias, c);
-    f[0] += t.x; f[1] += t.y; f[2] += t.z; f[3] += t.w;
-  }
-  if (!kQkv) {
-    activate_any(f, a.act);
-    if (a.gate && ok) {
-      const float4 t = load4<kBF16>(a.gate, b * a.gate_b + c);
-      f[0] *= t.x; f[1] *= t.y; f[2] *= t.z; f[3] *= t.w;
+__device__ __forceinline__ SkinnyLane skinny_lane(const LinearArgs& a, const HeadArgs& head, int c) {
+  SkinnyLane s;
+  s.ok = c < a.C;
+  const int cc = s.ok ? c : 0;
+  s.part = cc < a.part_cols ? 0 : cc / a.part_cols;
+  const int pc = cc - s.part * a.part_cols;
+  s.bias = a.bias ? load4<kBF16>(a.bias, cc) : make_float4(0.f, 0.f, 0.f, 0.f);
+  s.gain = make_float4(1.f, 1.f, 1.f, 1.f);
+  s.gate = s.residual = nullptr;
+  s.r_b = s.r_n = s.gate_b = 0;
+  s.l = s.d = 0;
+  if (kQkv) {
+    const int h = pc / head.D;
+    s.d = pc - h * head.D;
+    s.l = (threadIdx.x & 31) & (head.D / 4 - 1);
+    if (s.part < 2 && head.norm && head.weight[s.part] != nullptr)
+      s.gain = load4<kBF16>(head.weight[s.part], h * head.weight_h + s.d);
+  } else {
+    if (a.gate) {
+      if (a.gate_b == 0)
+        s.gain = load4<kBF16>(a.gate, cc);
+      else
+        s.gate = static_cast<const uint16_t*>(a.gate) + cc;
+      s.gate_b = a.gate_b;
     }
-    if (a.residual.ptr && ok) {
-      const float4 t = load4<kBF16>(a.residual.ptr, row_offset(a.residual, b, n, c));
-      f[0] += t.x; f[1] += t.y; f[2] += t.z; f[3] += t.w;
+    if (a.residual.ptr) {
+      s.residual = static_cast<const uint16_t*>(a.residual.ptr) + row_offset(a.residual, 0, 0, cc);
+      s.r_b = a.residual.b;
+      s.r_n = a.residual.n;
+    }
+  }
+  const RowView& y = a.y[s.part];
+  s.y = static_cast<uint16_t*>(const_cast<void*>(y.ptr)) + row_offset(y, 0, 0, pc);
+  s.y_b = y.b;
+  s.y_n = y.n;
+  return s;
+}
+
+// One token's 4 columns: bias, then act/gate/residual or the head's norm and rotation, the store.
+template <bool kBF16, bool kQkv>
+__device__ __forceinline__ void skinny_finish(const HeadArgs& head, int act, const SkinnyLane& t,
+                                              float4 s, int b, int n) {
+  float f[4] = {s.x + t.bias.x, s.y + t.bias.y, s.z + t.bias.z, s.w + t.bias.w};
+  if (!kQkv) {
+    activate_any(f, act);
+    float4 g = t.gain;
+    if (t.gate) g = load4<kBF16>(t.gate, b * t.gate_b);
+    f[0] *= g.x; f[1] *= g.y; f[2] *= g.z; f[3] *= g.w;
+    if (t.residual) {
+      const float4 r = load4<kBF16>(t.residual, b * t.r_b + n * t.r_n);
+      f[0] += r.x; f[1] += r.y; f[2] += r.z; f[3] += r.w;
     }
   } else {
     // a head lies across 16 lanes (D = 64) or the warp (D = 128)
-    const int lane = threadIdx.x & 31;
-    const int lanes = head.D / 4, l = lane & (lanes - 1);
-    const int h = pc / head.D, d = pc - h * head.D;
-    const bool turned_part = ok && part < 2;
+    const bool turned_part = t.ok && t.part < 2;
     if (head.norm) {
       float ss = f[0] * f[0] + f[1] * f[1] + f[2] * f[2] + f[3] * f[3];
-      for (int o = lanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      for (int o = head.D / 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       if (turned_part) {
         const float r = __frsqrt_rn(fmaf(ss, head.inv_d, head.eps));
-        float4 t = make_float4(1.f, 1.f, 1.f, 1.f);
-        if (head.weight[part]) t = load4<kBF16>(head.weight[part], h * head.weight_h + d);
-        f[0] *= r * t.x; f[1] *= r * t.y; f[2] *= r * t.z; f[3] *= r * t.w;
+        f[0] *= r * t.gain.x; f[1] *= r * t.gain.y; f[2] *= r * t.gain.z; f[3] *= r * t.gain.w;
       }
     }
     if (head.table) {
       const float* cs = head.table + b * head.table_b + (long long)n * head.rot;
-      const bool turned = turned_part && d < head.rot;
+      const bool turned = turned_part && t.d < head.rot;
       if (head.halves) {
         const int half = head.rot / 8;                   // lanes of one half of the pairs
-        const int partner = (lane - l) + (l < half ? l + half : (l < 2 * half ? l - half : l));
+        const int first = (int)(threadIdx.x & 31) - t.l;
+        const int partner = first + (t.l < half ? t.l + half : (t.l < 2 * half ? t.l - half : t.l));
         float g[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) g[i] = __shfl_sync(0xffffffffu, f[i], partner);
         if (turned) {
-          const bool low = l < half;
-          const float4* c4 = reinterpret_cast<const float4*>(cs + 8 * (low ? l : l - half));
+          const bool low = t.l < half;
+          const float4* c4 = reinterpret_cast<const float4*>(cs + 8 * (low ? t.l : t.l - half));
           const float4 t0 = __ldg(c4), t1 = __ldg(c4 + 1);
           const float sign = low ? -1.f : 1.f;
           f[0] = fmaf(f[0], t0.x, g[0] * (sign * t0.y));
@@ -131,21 +170,18 @@ __device__ __forceinline__ void skinny_finish(const LinearArgs& a, const HeadArg
           f[3] = fmaf(f[3], t1.z, g[3] * (sign * t1.w));
         }
       } else if (turned) {
-        const float4 t = __ldg(reinterpret_cast<const float4*>(cs + d));
+        const float4 t4 = __ldg(reinterpret_cast<const float4*>(cs + t.d));
         const float x0 = f[0], y0 = f[1], x1 = f[2], y1 = f[3];
-        f[0] = fmaf(x0, t.x, -y0 * t.y);
-        f[1] = fmaf(x0, t.y, y0 * t.x);
-        f[2] = fmaf(x1, t.z, -y1 * t.w);
-        f[3] = fmaf(x1, t.w, y1 * t.z);
+        f[0] = fmaf(x0, t4.x, -y0 * t4.y);
+        f[1] = fmaf(x0, t4.y, y0 * t4.x);
+        f[2] = fmaf(x1, t4.z, -y1 * t4.w);
+        f[3] = fmaf(x1, t4.w, y1 * t4.z);
       }
     }
   }
-  if (ok) {
-    const RowView& y = a.y[part];
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(const_cast<void*>(y.ptr)) +
-                              row_offset(y, b, n, pc)) =
+  if (t.ok)
+    *reinterpret_cast<uint2*>(t.y + b * t.y_b + n * t.y_n) =
         make_uint2(pack16<kBF16>(f[0], f[1]), pack16<kBF16>(f[2], f[3]));
-  }
 }
 
 template <bool kBF16, int kT, bool kQkv>
@@ -193,6 +229,8 @@ linear_skinny_kernel(const __grid_constant__ PairLinMaps maps,
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const SkinnyLane mine = skinny_lane<kBF16, kQkv>(a, args.head, c0 + 4 * lane);
+  const int N = a.N, rows = args.rows, act = a.act;
   // an earlier kernel gave up: skip the work (every CTA still meets its cluster below)
   const bool skip = *reinterpret_cast<volatile int*>(a.status) != 0;
 
@@ -276,41 +314,56 @@ linear_skinny_kernel(const __grid_constant__ PairLinMaps maps,
 
   // every CTA of the cluster has its partial sums in shared memory
   __syncthreads();
-  cluster_sync_all();
+  if (splits > 1) cluster_sync_all();
   if (!skip && !*abort_flag) {
-    const int tokens = min(kT, args.rows - t0);
-    const uint32_t mine = smem_u32(part) + (uint32_t)lane * 16u;
-    const bool run_on = args.rows != a.N;              // rows go through all branches
-    // two tokens at a time, all their partial sums in flight together
+    const int tokens = min(kT, rows - t0);
     const int step = splits * (kSkinnyThreads / 32);
-    for (int t = rank + splits * warp; t < tokens; t += 2 * step) {
-      const bool two = t + step < tokens;
-      float4 v[2][8];
+    const int first = rank + splits * warp;
+    float4* sums = reinterpret_cast<float4*>(part) + lane;     // token t: sums[t * 32]
+    // a warp's tokens: the sums over the cluster, into this CTA's own place for the token (which
+    // no other CTA reads); the partial sums of one token, or of two where a warp has several, in
+    // flight together
+    constexpr int kAhead = kT >= 128 ? 2 : 1;
+    if (splits > 1) {
+      const uint32_t here = smem_u32(sums);
+      for (int t = first; t < tokens; t += kAhead * step) {
+        float4 v[kAhead][8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        if (r < splits) {
-          const uint32_t peer = mapa_shared(mine, (uint32_t)r);
-          v[0][r] = ld_cluster_f4(peer + (uint32_t)t * 512u);
-          if (two) v[1][r] = ld_cluster_f4(peer + (uint32_t)(t + step) * 512u);
+        for (int r = 0; r < 8; ++r) {
+          if (r < splits) {
+            const uint32_t peer = mapa_shared(here, (uint32_t)r);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+              if (t + i * step < tokens) v[i][r] = ld_cluster_f4(peer + (uint32_t)(t + i * step) * 512u);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (t + i * step >= tokens) break;
+          float4 s = v[i][0];
+#pragma unroll
+          for (int r = 1; r < 8; ++r)
+            if (r < splits) {
+              s.x += v[i][r].x; s.y += v[i][r].y; s.z += v[i][r].z; s.w += v[i][r].w;
+            }
+          sums[(t + i * step) * 32] = s;
         }
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (i == 1 && !two) break;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < splits) {
-            s.x += v[i][r].x; s.y += v[i][r].y; s.z += v[i][r].z; s.w += v[i][r].w;
-          }
-        const int row = t0 + t + i * step;
-        const int b = run_on ? row / a.N : z;
-        skinny_finish<kBF16, kQkv>(a, args.head, s, b, run_on ? row - b * a.N : row, c0 + 4 * lane);
-      }
+    }
+    // then each token by itself
+    const bool run_on = rows != N;                     // rows go through all branches
+#pragma unroll kAhead
+    for (int t = first; t < tokens; t += step) {
+      const int row = t0 + t;
+      const int b = run_on ? row / N : z;
+      skinny_finish<kBF16, kQkv>(args.head, act, mine, sums[t * 32], b, run_on ? row - b * N : row);
     }
   }
   // no CTA leaves while its partial sums may still be read
-  cluster_sync_all();
+  if (splits > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) atomicExch(a.status, 1);
   if (warp == 1) {
     tc_fence_after();

@@ -233,12 +233,19 @@ int launch_skinny(const DeviceInfo& dev, SkinnyArgs p, int zs, tara_dtype dt, cu
       (rc = encode_weights(dev, &maps.w, dt, a.w, a.C, a.K, 128)) != TARA_OK)
     return rc;
   const long long c_tiles = ((long long)a.C + 127) / 128, t_tiles = ((long long)p.rows + kT - 1) / kT;
-  // K is split so that the CTAs fill whole rounds of those that run together; a CTA's
-  // start and end cost about as much as 8 of its K steps
-  const long long tiles = c_tiles * t_tiles * zs, slots = (long long)S::kCtas * dev.sms, steps = (a.K + 63) / 64;
-  long long best = 0;
+  // The split of K by the estimated time, in K steps of a CTA by itself.  CTAs that share an SM
+  // wait for memory much of the time: two of them take about 1.4 times as long as one.  Each CTA
+  // an SM runs costs about 4 steps beyond its own (start, the join over the cluster, the end).
+  // (7,168 -> 7,168, 1 row: 1 to 8 CTAs a tile take 36, 22, 16 and 20 us; 1,024 -> 4,096, 128 rows:
+  // 11.7, 10.8, 9.4 and 13.7; 4,096 -> 1,024, 1 row: 18.7, 12.2, 8.5 and 6.7.)
+  const long long tiles = c_tiles * t_tiles * zs, steps = (a.K + 63) / 64;
+  const double sms = dev.sms, room = (double)S::kCtas * dev.sms;
+  double best = 0.0;
   for (int s = 1; s <= 8 && s <= steps; s *= 2) {
-    const long long cost = (tiles * s + slots - 1) / slots * ((steps + s - 1) / s + 8);
+    const double ctas = (double)(tiles * s);
+    const double share = std::max(1.0, 0.7 * std::min(ctas, room) / sms);
+    const double cost = std::ceil(ctas / room) * std::ceil((double)steps / s) * share +
+                        4.0 * std::ceil(ctas / sms);
     if (s == 1 || cost < best) {
       best = cost;
       p.splits = s;
