@@ -235,14 +235,16 @@ rope_table_kernel(const float* __restrict__ pos, long long n_rows,
 // ---------------------------------------------------------------------------------------
 // norm_rope_kernel: a row of one head lies across LANES lanes, 8 elements a lane
 // ---------------------------------------------------------------------------------------
-// HBM-bound: every element of q and k is read and written once, ~10 operations each.  A warp
+// HBM-bound: every element of q and k is read and written once, ~10 operations each (56 heads x
+// 107,126 x 128 bf16: 960 to 990 us, 6.3 to 6.46 TB/s of a copy's 6.56; walking pointers and packed
+// fp32 took the last 4% off).  A warp
 // keeps 32/LANES tokens and walks heads, so a token's (cos, sin) pairs are read once for all
 // the heads of a CTA and stay in registers, and kBatch heads' loads are in flight per lane.
 //
 // Which 8 columns a lane holds: with interleaved pairs 8 consecutive ones.  With half-split
 // pairs lane l < R/8 holds [4l, 4l + 4) and [R/2 + 4l, R/2 + 4l + 4), so that both columns of a
 // pair are in one lane and no exchange between lanes is needed (two 8-byte accesses instead of
-// one of 16 bytes; exchanging the halves by shuffles measured 1,189 us where this takes 1,076);
+// one of 16 bytes; exchanging the halves by shuffles measured 1,189 us where this took 1,076);
 // the lanes behind hold the columns that do not turn, 8 consecutive ones each.
 struct NormRopeTensor {
   const void* in;
@@ -263,6 +265,8 @@ struct NormRopeArgs {
 };
 
 constexpr int kNormRopeThreads = 256;
+
+__device__ __forceinline__ uint64_t both2(float c) { return f32x2_pack(c, c); }
 
 template <typename T, int LANES, bool kHalves>
 __global__ void __launch_bounds__(kNormRopeThreads)
@@ -296,47 +300,63 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   const NormRopeTensor& t = a.t[which];
   const int h0 = (blockIdx.y - which * a.chunks) * a.heads_per_cta;
   const int h1 = min(h0 + a.heads_per_cta, a.H);
-  const T* in = static_cast<const T*>(t.in) + b * t.in_b + n * t.in_n;
-  T* out = static_cast<T*>(t.out) + b * t.out_b + n * t.out_n;
-  const T* weight = static_cast<const T*>(t.weight);
+  // strides and pointers in registers: the loop walks them from head to head
+  const long long in_h = t.in_h, out_h = t.out_h, weight_h = a.weight_h;
+  const T* in = static_cast<const T*>(t.in) + b * t.in_b + n * t.in_n + h0 * in_h;
+  T* out = static_cast<T*>(t.out) + b * t.out_b + n * t.out_n + h0 * out_h;
   auto load8 = [&](Vec8<T>& v, const T* row) {
     if (kHalves)
       v.load(row + c0, row + c1);
     else
       v.load(row + c0);
   };
-  const bool weighted = a.norm && t.weight != nullptr && live;
-  float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-  if (weighted) {
+  const bool norm = a.norm;
+  const T* weight = static_cast<const T*>(t.weight);
+  const bool weighted = norm && weight != nullptr && live;
+  // the weights as packed pairs; those of each head are loaded in the loop
+  uint64_t w[4] = {both2(1.f), both2(1.f), both2(1.f), both2(1.f)};
+  auto load_weight = [&](const T* p) {
     Vec8<T> wv;
-    load8(wv, weight);
-    wv.unpack(w);
-  }
+    float f[8];
+    load8(wv, p);
+    wv.unpack(f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = f32x2_pack(f[2 * j], f[2 * j + 1]);
+  };
+  const bool per_head = weighted && weight_h != 0;
+  if (weighted && !per_head) load_weight(weight);
+  const float eps = a.eps, inv_d = a.inv_d;
 
-  for (int h = h0; h < h1; h += kBatch) {
+  for (int left = h1 - h0, h = h0; left > 0; left -= kBatch, h += kBatch) {
     Vec8<T> v[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (live && h + i < h1) load8(v[i], in + (h + i) * t.in_h);
+    for (int i = 0; i < kBatch; ++i) {
+      if (live && i < left) load8(v[i], in);
+      in += in_h;
+    }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      if (h + i >= h1) break;                             // the same for the whole warp
+      if (i >= left) break;                               // the same for the whole warp
       float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       if (live) v[i].unpack(x);
-      if (a.norm) {
-        float ss = 0.f;
+      if (norm) {
+        uint64_t p[4], ss = 0;                            // (0, 0)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float r = __frsqrt_rn(fmaf(ss, a.inv_d, a.eps));
-        if (a.weight_h != 0 && weighted) {
-          Vec8<T> wv;
-          load8(wv, weight + (h + i) * a.weight_h);
-          wv.unpack(w);
+        for (int j = 0; j < 4; ++j) {
+          p[j] = f32x2_pack(x[2 * j], x[2 * j + 1]);
+          ss = f32x2_fma(p[j], p[j], ss);
         }
+        float s0, s1;
+        f32x2_unpack(ss, s0, s1);
+        s0 += s1;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= r * w[j];
+        for (int o = LANES / 2; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+        const float r = __frsqrt_rn(fmaf(s0, inv_d, eps));
+        if (per_head) load_weight(weight + (h + i) * weight_h);
+        const uint64_t rr = both2(r), zero = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          f32x2_unpack(f32x2_fma(p[j], f32x2_fma(rr, w[j], zero), zero), x[2 * j], x[2 * j + 1]);
       }
       if (turned) {
 #pragma unroll
@@ -350,12 +370,12 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
         }
       }
       if (live) {
-        T* row = out + (h + i) * t.out_h;
         if (kHalves)
-          Vec8<T>::store(row + c0, row + c1, x);
+          Vec8<T>::store(out + c0, out + c1, x);
         else
-          Vec8<T>::store(row + c0, x);
+          Vec8<T>::store(out + c0, x);
       }
+      out += out_h;
     }
   }
 }
