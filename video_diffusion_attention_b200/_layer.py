@@ -121,6 +121,8 @@ def _elsewhere(t, stream):
         raise ValueError("expected CUDA tensors")
     if stream is None and torch.cuda.current_device() == t.get_device():
         return None
+    if stream is not None and stream.device != t.device:
+        raise ValueError("the stream and the tensors must be on one device")
     stack = contextlib.ExitStack()
     stack.enter_context(torch.cuda.device(t.device))
     if stream is not None:

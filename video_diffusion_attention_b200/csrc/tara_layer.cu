@@ -262,9 +262,11 @@ int launch_skinny(const DeviceInfo& dev, SkinnyArgs p, int zs, tara_dtype dt, cu
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_skinny_kernel<kBF16, kT, kQkv>, maps, p) == cudaSuccess
-             ? TARA_OK
-             : TARA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, linear_skinny_kernel<kBF16, kT, kQkv>, maps, p) != cudaSuccess) {
+    cudaGetLastError();   // a refused launch leaves nothing behind for the next call's check
+    return TARA_ERR_CUDA;
+  }
+  return TARA_OK;
 }
 
 template <bool kBF16, bool kQkv>
@@ -356,7 +358,7 @@ int run_linear(LinearArgs a, const HeadArgs* head, tara_dtype dt, cudaStream_t s
     }
   }
   // 512 x 256 reads a quarter less through L2 than 256 x 256, but its accumulators fill tensor
-  // memory, so part of every epilogue is exposed (about 7,000 cycles).  Long calls run at the
+  // memory, so part of every epilogue is exposed (about 5,000 cycles).  Long calls run at the
   // power cap, where the saved traffic counts for more: 107,126 x 7,168 -> 7,168 back to back
   // takes 8.7 ms against 9.3; with 1,024 input columns the exposed epilogue loses (1.05 against
   // 0.69 ms).
