@@ -231,6 +231,9 @@ LINEAR_CASES = [
     (5, 3, 1024, 256, "bf16", 8, "bgr", "gelu", 2),
     (2, 31, 2048, 128, "bf16", 16, "bgr", None, None),
     (1, 255, 1024, 640, "fp16", 0, "r", "gelu_tanh", None),
+    (1, 255, 2304, 640, "fp16", 0, "r", "gelu_tanh", None),     # streamed with 256 tokens a tile
+    (3, 70, 2048, 264, "bf16", 16, "bgr", "silu", None),
+    (1, 129, 4096, 136, "bf16", 0, "b", None, None),
     (1, 7, 64, 24000, "bf16", 0, "bg", None, None),
     (2, 5300, 128, 4608, "fp16", 2, "r", None, 36),
     (1, 1, 1, 1, "fp32", 0, "bgr", "gelu", None),
@@ -331,6 +334,8 @@ QKV_CASES = [
     (3, 20, 1024, 3, 64, "bf16", 8, True, True, "head", (48,), True),
     (1, 17, 1032, 4, 128, "fp16", 0, True, True, "shared", (40,), False),
     (2, 120, 512, 2, 128, "bf16", 0, True, False, None, (96,), True),
+    (2, 120, 2048, 2, 128, "bf16", 0, True, True, "head", (96,), True),
+    (1, 250, 2056, 3, 64, "fp16", 0, True, True, "shared", (64,), False),
     (1, 16, 192, 40, 64, "bf16", 0, False, True, "shared", (16, 24, 24), False),
     (1, 2100, 128, 7, 128, "fp16", 0, True, True, "shared", (16, 56, 56), True),
     (1, 8200, 64, 17, 128, "bf16", 0, True, True, "head", (44, 42, 42), False),

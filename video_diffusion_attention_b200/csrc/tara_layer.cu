@@ -279,8 +279,13 @@ int launch_skinny_rows(const DeviceInfo& dev, const SkinnyArgs& p, int zs, tara_
   return launch_skinny<kBF16, 256, kQkv>(dev, p, zs, dt, stream);
 }
 
-// Rows up to which the weight-streaming kernel is taken.
-constexpr long long kSkinnyRows = 256;
+// Whether the kernel that streams W takes a call of `rows` rows: up to 128 (7,168 -> 7,168, 128
+// rows: 26 us against 34), and up to 256 where the output is too narrow to give the pair kernel's
+// tiles to many SMs but K is long enough to split (4,096 -> 1,024, 129 to 256 rows: 11 to 14 us
+// against 21; at 7,168 -> 7,168 31 to 38 against 35, at 7,168 -> 21,504 115 to 130 against 72 to 77).
+bool streams_weights(long long rows, int C, int K, int sms) {
+  return rows <= 128 || (rows <= 256 && (C + 127LL) / 128 * 8 <= sms && K >= 2048);
+}
 
 // head: the norm and rotation of a projection's q and k, or nullptr.
 int run_linear(LinearArgs a, const HeadArgs* head, tara_dtype dt, cudaStream_t stream) {
@@ -315,7 +320,7 @@ int run_linear(LinearArgs a, const HeadArgs* head, tara_dtype dt, cudaStream_t s
   if (rc != TARA_OK) return rc;
   a.status = dev.status;
   const bool heads = head != nullptr;
-  if ((long long)a.B * a.N <= kSkinnyRows) {
+  if (streams_weights((long long)a.B * a.N, a.C, a.K, dev.sms)) {
     SkinnyArgs p{};
     p.lin = a;
     if (head) p.head = *head;
