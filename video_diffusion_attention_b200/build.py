@@ -26,6 +26,7 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC,-O2",
     "-shared", "-cudart", "static",
     "--expt-relaxed-constexpr",
+    "--threads", "4",            # the translation units side by side
 ]
 
 
