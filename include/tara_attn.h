@@ -455,7 +455,9 @@ int tara_linear(const tara_view* x, const void* w, const tara_epilogue* e, tara_
 /* The projection in front of the attention: [q | k | v] = x W^T + bias, q and k through the
  * norm and rotation of tara_qk_norm_rope, all three written as views [B][H][N][D] (for instance
  * rows of the packed tensors tara_attn_forward takes).
- *   w : device [3*H*D][C_in]: the rows of q's heads, then k's, then v's.  bias [3*H*D] or NULL.
+ *   w : device [3*H*D][C_in], H and D those of the view q: the rows of q's heads, then k's, then
+ *       v's.  bias [3*H*D] or NULL.  The call reads that many rows; their number is the caller's
+ *       to see to (the library knows w and bias as pointers only).
  *   p : NULL: no norm and no rotation.
  * bf16/fp16: D = 64 or 128; one kernel, the norm on the fp32 accumulators, one rounding.
  * fp32: D as in tara_qk_norm_rope, two kernels.  Other requirements and errors as for

@@ -318,6 +318,48 @@ def test_binding_refuses_host_tensors():
             f()
 
 
+class NoCalls:
+    """A library of which nothing may be called."""
+
+    def __getattr__(self, name):
+        raise AssertionError("%s was called" % name)
+
+
+@pytest.mark.parametrize("shape", [
+    (2, 4, 30, 64),      # more heads than w has rows
+    (2, 1, 30, 64),      # fewer
+    (2, 2, 30, 128),     # longer heads
+    (2, 4, 30, 32),      # the same columns in other heads
+    (2, 1, 30, 128),     # the same columns in one head
+    (2, 30, 128),        # token-major
+    (2, 30, 64),         # token-major, one head
+    (2, 2, 31, 64),      # another number of tokens
+    (1, 2, 30, 64),      # one branch
+])
+@pytest.mark.parametrize("which", [0, 1, 2])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_binding_refuses_outputs_unlike_the_projection(monkeypatch, dtype, which, shape):
+    # The library sees w as a pointer and takes its rows from the outputs: outputs of other sizes
+    # would read behind w, bias and weights.  Refused before any library call (host tensors here).
+    import torch
+    from video_diffusion_attention_b200 import _layer
+    monkeypatch.setattr(_layer, "_elsewhere", lambda t, stream: None)
+    monkeypatch.setattr(_layer, "_current_stream", lambda t: 0)
+    monkeypatch.setattr(_layer, "load_library", NoCalls)
+    dt = getattr(torch, dtype)
+    heads, D, K = 2, 64, 96
+    x, w = torch.zeros(2, 30, K, dtype=dt), torch.zeros(3 * heads * D, K, dtype=dt)
+    out = [torch.zeros(2, heads, 30, D, dtype=dt) for _ in range(3)]
+    out[which] = torch.zeros(shape, dtype=dt)
+    with pytest.raises(ValueError):
+        T.qkv_project(x, w, heads, bias=torch.zeros(3 * heads * D, dtype=dt),
+                      q_weight=torch.ones(heads, D, dtype=dt), out=out)
+    with pytest.raises(ValueError):
+        T.qkv_project(x, w, heads, out=[torch.zeros(shape, dtype=dt)] * 3)
+    with pytest.raises(ValueError):
+        T.qkv_project(x, w, heads, out=out[:2])
+
+
 def test_struct_sizes_match_the_header(tmp_path):
     # the ctypes layouts against the C compiler's
     import os

@@ -313,6 +313,10 @@ def qkv_project(x, w, heads: int, bias=None, q_weight=None, k_weight=None, eps: 
         q, k, v = out
         _same_device(x, q, k, v)
         qv, kv, vv = _view(q), _view(k), _view(v)
+        # the library takes w's rows, and those of bias and weights, from the outputs' sizes
+        for o in (qv, kv, vv):
+            if (o.B, o.H, o.N, o.D) != (B, heads, N, D):
+                raise ValueError("out must be three [%d][%d][%d][%d] tensors" % (B, heads, N, D))
     _check(load_library().tara_qkv_project(
         ctypes.byref(xv), w.data_ptr(), bias_ptr, p, ctypes.byref(qv), ctypes.byref(kv),
         ctypes.byref(vv), _current_stream(x)), "tara_qkv_project")
