@@ -448,7 +448,7 @@ typedef struct {
  * _TOO_LARGE, TARA_ERR_CUDA.  No workspace and no atomics: calls on several streams, captured or
  * not, do not touch one another, and the same call gives the same bits.  Asynchronous on
  * `stream`.  The 16-bit kernels bound their waits like the attention kernels: while the status
- * word of tara_device_status is set they skip their work.                                  */
+ * word of tara_device_status is set they write nothing (one decision a cluster).            */
 int tara_linear(const tara_view* x, const void* w, const tara_epilogue* e, tara_view* y,
                 void* stream);
 

@@ -570,6 +570,32 @@ def test_launches_skip_while_the_status_word_is_set(N):
     close(T.linear(x, w, out=y), value, bound, "bf16")
 
 
+@pytest.mark.parametrize("N,K,C", [(1, 4096, 1024), (40, 2048, 512), (100, 512, 2048), (3, 64, 384)])
+def test_a_status_word_that_changes_meanwhile(N, K, C):
+    # the word is set by a kernel on another stream, and read and cleared by the host, while calls
+    # of few rows start: every 128 columns of an output are either all there or untouched
+    x, w, _ = linear_inputs(1, N, K, C, "bf16", 0, "")
+    want = T.linear(x, w)
+    assert T.device_status() == 0
+    outs = torch.full((6, 40, 1, N, C), 3.0, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    here, there = torch.cuda.Stream(), torch.cuda.Stream()
+    seen = []
+    for ys in outs:
+        T.selftest_wait(200, arrive=False, stream=there)
+        for y in ys:
+            T.linear(x, w, out=y, stream=here)
+        seen.append(T.device_status(stream=there))       # waits for that stream only
+    torch.cuda.synchronize()
+    T.device_status()
+    assert -10 in seen
+    tiles = outs.view(-1, N, C // 128, 128)
+    done = (tiles == want.view(N, C // 128, 128)).all(-1).all(1)
+    untouched = (tiles == 3.0).all(-1).all(1)
+    assert bool((done | untouched).all())
+    assert torch.equal(T.linear(x, w), want) and T.device_status() == 0
+
+
 def test_the_binding_refuses():
     x, w, o = linear_inputs(1, 6, 64, 128, "bf16", 0, "bgr")
     bad = [

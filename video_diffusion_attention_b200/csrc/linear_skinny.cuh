@@ -64,6 +64,12 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // 4 consecutive 16-bit values <-> fp32.
 template <bool kBF16>
 __device__ __forceinline__ float4 load4(const void* p, long long i) {
@@ -76,7 +82,7 @@ __device__ __forceinline__ float4 load4(const void* p, long long i) {
 // CTA's 128 columns): parameters in registers, addresses as base and strides.  Gathered while the
 // products run; computed per token it made each take 800 cycles.
 struct SkinnyLane {
-  bool ok;                  // the columns exist
+  bool ok;                  // the columns exist and are to be stored
   int part, l, d;           // output part; lane and column within the head (projection)
   float4 bias, gain;        // gain: gate (when shared by the branches) or norm weight
   uint16_t* y;
@@ -201,6 +207,7 @@ linear_skinny_kernel(const __grid_constant__ PairLinMaps maps,
   uint64_t* acc_full = empty + NS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* skip_flag = abort_flag + 1;            // rank 0's holds for the whole cluster
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int splits = args.splits;
@@ -229,13 +236,17 @@ linear_skinny_kernel(const __grid_constant__ PairLinMaps maps,
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const SkinnyLane mine = skinny_lane<kBF16, kQkv>(a, args.head, c0 + 4 * lane);
+  SkinnyLane mine = skinny_lane<kBF16, kQkv>(a, args.head, c0 + 4 * lane);
   const int N = a.N, rows = args.rows, act = a.act;
-  // an earlier kernel gave up: skip the work (every CTA still meets its cluster below)
-  const bool skip = *reinterpret_cast<volatile int*>(a.status) != 0;
+
+  // Whether an earlier kernel gave up, read once a cluster: the word may change while this kernel
+  // runs, and warps or CTAs that read it by themselves could take different ways (a CTA would
+  // leave with its copies in flight, or sum partial sums nobody wrote).  All of them load and
+  // multiply; the flag only withholds the stores, so its latency is hidden.
+  if (rank == 0 && threadIdx.x == 64) *skip_flag = *reinterpret_cast<volatile int*>(a.status);
 
   if (warp == 0) {
-    if (lane == 0 && !skip) {
+    if (lane == 0) {
       tma_prefetch_desc(&maps.w);
       tma_prefetch_desc(&maps.x);
       const int xD = a.x.D;
@@ -267,7 +278,7 @@ linear_skinny_kernel(const __grid_constant__ PairLinMaps maps,
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     }
   } else if (warp == 1) {
-    if (lane == 0 && !skip) {
+    if (lane == 0) {
       constexpr uint32_t idesc = make_idesc_f16(128, kT, kBF16, false);
       const uint64_t wd0 = make_sdesc_sw128(smem_u32(smem), 16, 1024);
       const uint64_t xd0 = make_sdesc_sw128(smem_u32(smem + S::kWBytes), 16, 1024);
@@ -292,7 +303,7 @@ linear_skinny_kernel(const __grid_constant__ PairLinMaps maps,
       volatile int no_abort = 0;
       if (*abort_flag) mbar_wait(acc_full, 0, &no_abort, kLinDrainNs);
     }
-  } else if (!skip) {
+  } else {
     if (mbar_wait_warp(acc_full, 0, abort_flag)) {
       tc_fence_after();
       const int q = warp & 3;                          // TMEM lane quarter
@@ -315,7 +326,9 @@ linear_skinny_kernel(const __grid_constant__ PairLinMaps maps,
   // every CTA of the cluster has its partial sums in shared memory
   __syncthreads();
   if (splits > 1) cluster_sync_all();
-  if (!skip && !*abort_flag) {
+  if (!*abort_flag) {
+    const int skip =
+        ld_cluster_s32(mapa_shared(smem_u32(const_cast<const int*>(skip_flag)), 0));
     const int tokens = min(kT, rows - t0);
     const int step = splits * (kSkinnyThreads / 32);
     const int first = rank + splits * warp;
@@ -351,6 +364,7 @@ linear_skinny_kernel(const __grid_constant__ PairLinMaps maps,
       }
     }
     // then each token by itself
+    mine.ok = mine.ok && skip == 0;
     const bool run_on = rows != N;                     // rows go through all branches
 #pragma unroll kAhead
     for (int t = first; t < tokens; t += step) {
