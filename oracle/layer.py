@@ -89,6 +89,27 @@ def _silu(v):
 ACTS = {"none": lambda v: v, "gelu": _gelu, "gelu_tanh": _gelu_tanh, "silu": _silu}
 
 
+def activation(v, act):
+    """Value of an activation in a form that keeps its relative accuracy far below zero, and the
+    relative error of an fp32 evaluation of it that does the same (its scale is |act(v)|).
+
+    Counted in units of 2^-24: two dozen for exponential, reciprocal and the products around them
+    (and a polynomial of ten terms, erf form).  Below zero the result is proportional to exp(-y),
+    and each rounding of y is worth |y| units of it (silu: y = |v|, tanh form: y = 2|u|, erf form:
+    y = v^2/2); y beyond 100 is left out, where exp(-y) is no normal fp32 number.  Above zero
+    the exponential is added to 1, and y exp(-y) < 0.4."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        if act == "silu":
+            y, value, per_y, units = v, v / (1.0 + np.exp(-v)), 2, 24
+        elif act == "gelu_tanh":
+            y = 2.0 * math.sqrt(2.0 / math.pi) * (v + 0.044715 * v ** 3)
+            value, per_y, units = v / (1.0 + np.exp(-y)), 6, 24
+        else:
+            y, per_y, units = v * v / 2.0, 4, 48
+            value = 0.5 * v * np.vectorize(math.erfc)(-v / math.sqrt(2.0))
+        return value, U32 * (units + per_y * np.where(v < 0, np.minimum(np.abs(y), 100.0), 1.0))
+
+
 def product(x, w, bias):
     """x [M][K] w [C][K]^T + bias and its fp32 bound: K products summed in any order, with the
     truncating adds of a tensor core (one unit, not half, per add)."""

@@ -314,6 +314,41 @@ def test_linear_keeps_bad_rows_apart():
         assert not ok[3] and not ok[4] and int(ok.sum()) == N - 2
 
 
+TAILS = [-0.25, -1.0, -3.0, -5.0, -7.5, -8.0, -10.5, -12.75, -20.0, -41.0, -42.0, -50.0, -80.0, -100.0,
+         -1e4, -1e10, -1e16, -1e20, -1e25, -3e38, 0.0, 0.5, 5.0, 13.0, 60.0, 1e4, 1e20, 3e38]
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "gelu"])
+@pytest.mark.parametrize("N", [1, 300])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_activations_keep_their_tails(dtype, N, act):
+    # x picks one column of w, so the pre-activations are w's values exactly; every value lies
+    # beside an ordinary one, an infinity and a NaN (two columns may be worked on together)
+    v = torch.tensor(TAILS).to(DT[dtype]).float()
+    v = v[torch.isfinite(v)]
+    beside = [v, torch.ones_like(v), v, torch.full_like(v, float("nan")), v, torch.full_like(v, float("inf")),
+              v, torch.full_like(v, -float("inf"))]
+    cols = torch.stack(beside, 1).reshape(-1)
+    w = torch.zeros(len(cols), 64)
+    w[:, 7] = cols
+    x = torch.zeros(1, N, 64)
+    x[:, :, 7] = 1.0
+    y = T.linear(x.to(DT[dtype]).cuda(), w.to(DT[dtype]).cuda(), act=act)
+    assert T.device_status() == 0
+    got = np64(y)[0].reshape(N, len(v), 8)
+    value, rel = ref.activation(np64(v), act)
+    # fp32 results below its smallest normal number are cut to zero, the output's own steps end too
+    step = {"bf16": 2.0 ** -133, "fp16": 2.0 ** -24}[dtype]
+    bound = np.abs(value) * rel + np.abs(np64(v)) * 2.0 ** -125
+    tol = bound + torch.finfo(DT[dtype]).eps / 2 * (np.abs(value) + bound) + step / 2
+    for i in (0, 2, 4, 6):
+        assert np.all(np.abs(got[:, :, i] - value) <= tol), (i, got[0, :, i], value)
+    one, rel1 = ref.activation(np.ones(1), act)
+    assert np.all(np.abs(got[:, :, 1] - one) <= one * (rel1 + torch.finfo(DT[dtype]).eps))
+    assert np.all(np.isnan(got[:, :, 3])) and np.all(np.isposinf(got[:, :, 5]))
+    assert not np.any(np.isinf(got[:, :, 7]))            # -infinity times 0, or the limit
+
+
 # ---------------------------------------------------------------------------------------
 # qkv_project
 # ---------------------------------------------------------------------------------------

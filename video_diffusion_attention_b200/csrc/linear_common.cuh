@@ -35,9 +35,9 @@ struct LinearArgs {
 
 // Activations on the fp32 accumulators (numbering of tara_act), two elements at a time in packed
 // fp32.  What bounds them in the epilogue is the special-function unit, 16 results a cycle and SM:
-// two reciprocals are taken as one, of the product (1.5 operations an element instead of 2;
-// operands are clamped so that the product stays finite and an infinity or NaN stays in its own
-// element), and the polynomial runs on packed FMAs.
+// two reciprocals are taken as one, of the product (1.5 operations an element instead of 2; what
+// goes into the product is bounded, so that it stays finite and an infinity or NaN stays in its
+// own element), and the polynomial runs on packed FMAs.
 __device__ __forceinline__ uint64_t both(float c) { return f32x2_pack(c, c); }
 __device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
   uint64_t d;
@@ -50,15 +50,16 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// v <- v / (1 + 2^x)
+// (v0, v1) <- v 2^x / (1 + 2^x).  x is cut off above 60, where the factor is 1 to fp32, so that the
+// product of two denominators stays finite; below, 2^x runs down to 0 and the result with it,
+// however large |v| is.  (A NaN in x counts as 60: it stays in its own v.)
 __device__ __forceinline__ void logistic_pair(float& v0, float& v1, uint64_t x) {
   float x0, x1, d0, d1;
   f32x2_unpack(x, x0, x1);
-  f32x2_unpack(f32x2_add(f32x2_pack(ex2_approx(fminf(x0, 60.f)), ex2_approx(fminf(x1, 60.f))),
-                         both(1.f)), d0, d1);
-  const float r = rcp_approx(d0 * d1);
-  v0 *= r * d1;
-  v1 *= r * d0;
+  const uint64_t e = f32x2_pack(ex2_approx(fminf(x0, 60.f)), ex2_approx(fminf(x1, 60.f)));
+  f32x2_unpack(f32x2_add(e, both(1.f)), d0, d1);
+  const uint64_t factor = f32x2_mul(f32x2_mul(e, f32x2_pack(d1, d0)), both(rcp_approx(d0 * d1)));
+  f32x2_unpack(f32x2_mul(f32x2_pack(v0, v1), factor), v0, v1);
 }
 
 template <int kAct>
@@ -91,10 +92,10 @@ __device__ __forceinline__ void activate_pair(float& v0, float& v1) {
     v1 *= v1 < 0.f ? h1 : 1.f - h1;
   } else if (kAct == 2) {
     // v/2 (1 + tanh u) = v / (1 + exp(-2u)), u = sqrt(2/pi) (v + 0.044715 v^3)
-    const uint64_t s = f32x2_fma(f32x2_mul(v, v), both(-0.10294324f), both(-2.30220819814f));
+    const uint64_t s = f32x2_fma(f32x2_mul(v, v), both(0.10294324f), both(2.30220819814f));
     logistic_pair(v0, v1, f32x2_mul(v, s));
   } else if (kAct == 3) {
-    logistic_pair(v0, v1, f32x2_mul(v, both(-1.44269504089f)));
+    logistic_pair(v0, v1, f32x2_mul(v, both(1.44269504089f)));
   }
 }
 
