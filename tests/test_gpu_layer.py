@@ -320,7 +320,7 @@ TAILS = [-0.25, -1.0, -3.0, -5.0, -7.5, -8.0, -10.5, -12.75, -20.0, -41.0, -42.0
 
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh", "gelu"])
 @pytest.mark.parametrize("N", [1, 300])
-@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 def test_activations_keep_their_tails(dtype, N, act):
     # x picks one column of w, so the pre-activations are w's values exactly; every value lies
     # beside an ordinary one, an infinity and a NaN (two columns may be worked on together)
@@ -338,7 +338,7 @@ def test_activations_keep_their_tails(dtype, N, act):
     got = np64(y)[0].reshape(N, len(v), 8)
     value, rel = ref.activation(np64(v), act)
     # fp32 results below its smallest normal number are cut to zero, the output's own steps end too
-    step = {"bf16": 2.0 ** -133, "fp16": 2.0 ** -24}[dtype]
+    step = {"bf16": 2.0 ** -133, "fp16": 2.0 ** -24, "fp32": 2.0 ** -149}[dtype]
     bound = np.abs(value) * rel + np.abs(np64(v)) * 2.0 ** -125
     tol = bound + torch.finfo(DT[dtype]).eps / 2 * (np.abs(value) + bound) + step / 2
     for i in (0, 2, 4, 6):

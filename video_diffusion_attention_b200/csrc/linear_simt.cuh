@@ -17,9 +17,10 @@ namespace tara {
 
 constexpr int kSimtLinThreads = 256;
 
-// The activations once more for single fp32 results, by CUDA's own functions.
+// The activations once more for single fp32 results, by CUDA's own functions (erfc, not 1 + erf,
+// which is 0 from v = -5.5 on, where v Phi(v) is -1e-7).
 __device__ __forceinline__ float simt_activate(float v, int act) {
-  if (act == 1) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  if (act == 1) return 0.5f * v * erfcf(v * -0.70710678118654752f);
   if (act == 2) return v / (1.0f + expf(-1.5957691216f * (v + 0.044715f * v * v * v)));
   if (act == 3) return v / (1.0f + expf(-v));
   return v;
