@@ -442,13 +442,15 @@ typedef struct {
  *   e : epilogue, NULL for none.  residual may be y itself (same ptr and strides).
  *   y : view with H*D = C_out columns (written); token-major or head-major.
  * One dtype throughout.  bf16/fp16: tensor cores; the D of every view a multiple of 8 (of 64
- * where its H > 1), no stride of x 0 (x may not be an expanded view; the residual may).  fp32: an exact CUDA-core kernel, any sizes, pointers 4-byte aligned and
- * strides free.  bias, gate 16-byte aligned, gate_stride a multiple of 16 bytes (16-bit types).
+ * where its H > 1), no stride of x 0 (x may not be an expanded view; the residual may).  fp32:
+ * an exact CUDA-core kernel, any sizes, pointers 4-byte aligned and strides free.  bias, gate
+ * 16-byte aligned, gate_stride a multiple of 16 bytes (16-bit types).
  * Errors: TARA_ERR_NULL, _SHAPE, _DTYPE, _PARAM (act, a stride, overlapping views), _ALIGN,
- * _TOO_LARGE, TARA_ERR_CUDA.  No workspace and no atomics: calls on several streams, captured or
- * not, do not touch one another, and the same call gives the same bits.  Asynchronous on
- * `stream`.  The 16-bit kernels bound their waits like the attention kernels: while the status
- * word of tara_device_status is set they write nothing (one decision a cluster).            */
+ * _TOO_LARGE (C_in above 2^31 - 256 among them), TARA_ERR_CUDA.  No workspace and no atomics:
+ * calls on several streams, captured or not, do not touch one another, and the same call gives
+ * the same bits.  Asynchronous on `stream`.  The 16-bit kernels bound their waits like the
+ * attention kernels (2 s, also for the products of one tile: C_in to about 10^8): while the
+ * status word of tara_device_status is set they write nothing (one decision a cluster).     */
 int tara_linear(const tara_view* x, const void* w, const tara_epilogue* e, tara_view* y,
                 void* stream);
 

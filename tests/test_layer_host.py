@@ -255,6 +255,25 @@ def test_qkv_project_refuses(lib):
     assert call_qkv(lib, stream_view(FAKE, 300, 256, f), FAKE2, None, None, *outs) == HEAD_DIM
 
 
+@pytest.mark.parametrize("K", [2 ** 31 - 1, 2 ** 31 - 8, 2 ** 31 - 64, 2 ** 31 - 248])
+@pytest.mark.parametrize("dtype", [B.TARA_FP32, B.TARA_BF16])
+@pytest.mark.parametrize("N", [1, 8, 9, 300])
+def test_input_columns_leave_room_for_a_step_of_the_kernels(lib, N, dtype, K):
+    # the kernels count input columns in int and step past the last one by less than 256; with
+    # fp32 one row may stand for all tokens (8 GB), so that such a call is possible
+    if dtype == B.TARA_BF16:
+        K -= K % 8
+    x = view(FAKE, dtype, (1, 1, N, K), (0, 0, 0 if dtype == B.TARA_FP32 else 1 << 31))
+    assert call_linear(lib, x, FAKE2, None, view(FAKE3, dtype, (1, 1, N, 8))) == TOO_LARGE
+    outs = [view(a, dtype, (1, 1, N, 64)) for a in (FAKE3, FAKE4, FAKE5)]
+    assert call_qkv(lib, x, FAKE2, None, None, *outs) == TOO_LARGE
+
+
+def test_input_columns_count_over_all_heads(lib):
+    heads = view(FAKE, B.TARA_BF16, (1, (1 << 25) - 1, 1, 64), (0, 64, 0))
+    assert call_linear(lib, heads, FAKE2, None, stream_view(FAKE3, 1, 8)) == TOO_LARGE
+
+
 # ---------------------------------------------------------------------------------------
 # positions
 # ---------------------------------------------------------------------------------------

@@ -89,16 +89,20 @@ RowView row_view(const tara_view& v) {
 }
 
 // A view of the linear layer: 16-bit views are read and written by 16-byte chunks, x by 64-column
-// boxes of a tensor map (whose strides may not be 0); the fp32 kernels take anything.
-int check_linear_view(const tara_view* v, bool out, bool mapped) {
+// boxes of a tensor map (whose strides may not be 0); the fp32 kernels take anything.  The kernels
+// count x's columns in int and step past the last one, by less than kLinearStep.
+constexpr int64_t kLinearStep = 256;
+
+int check_linear_view(const tara_view* v, bool out, bool is_x) {
   if (!v) return TARA_ERR_NULL;
   const int align = v->dtype == TARA_FP32 ? 0 : 16;
   const int rc = out ? check_out_view(v, align) : check_view(v, align);
   if (rc != TARA_OK) return rc;
+  if (is_x && (int64_t)v->H * v->D > ((int64_t)1 << 31) - kLinearStep) return TARA_ERR_TOO_LARGE;
   if (v->dtype == TARA_FP32) return TARA_OK;
   if (v->D % 8 != 0 || (v->H > 1 && v->D % 64 != 0)) return TARA_ERR_SHAPE;
-  if (mapped && ((v->B > 1 && v->stride_b == 0) || (v->H > 1 && v->stride_h == 0) ||
-                 (v->N > 1 && v->stride_n == 0)))
+  if (is_x && ((v->B > 1 && v->stride_b == 0) || (v->H > 1 && v->stride_h == 0) ||
+               (v->N > 1 && v->stride_n == 0)))
     return TARA_ERR_PARAM;
   return TARA_OK;
 }
