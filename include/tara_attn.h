@@ -382,6 +382,8 @@ typedef struct {
  *   pos   : device float array [n_rows][n_axes], finite; angles are formed in double
  *           precision, so far positions keep their phase (|angle| up to 2^31 radians).
  *   table : device float array [n_rows][R/2][2] (written), cos then sin; 16-byte aligned.
+ *           Every value is within 1e-7 + |angle| * 2^-51 of the exact one (root mean square
+ *           1.6e-8 to 1.7e-8 for positions up to 5e4; correctly rounded values have 1.4e-8).
  * Errors: TARA_ERR_NULL, TARA_ERR_SHAPE (n_rows < 1, a dim odd or < 2, R > 256 or not a
  * multiple of 4), TARA_ERR_PARAM (n_axes or theta), TARA_ERR_ALIGN (pos 4 bytes),
  * TARA_ERR_CUDA.  Asynchronous on `stream`.                                                */

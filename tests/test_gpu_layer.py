@@ -70,6 +70,18 @@ def test_rope_table(N, dims, theta, far):
     assert np.all(np.abs(got - want) <= tol), np.max(np.abs(got - want))
 
 
+@pytest.mark.parametrize("far", [0.0, 5e4, 2.0 ** 30])
+def test_rope_table_error_bound(far):
+    # The bound the header states: 1e-7 beside the error of the fp64 angle (2^-50 relative, the
+    # definition's own included).  Counted: the remainder rounded to fp32 below pi/4, 2^-25; the
+    # last fma of a series below 1, 2^-25; its inner terms below 2^-25.5; the series, 2^-29.
+    pos = positions(20000, 3, 77, far)
+    got = np64(T.rope_table(pos, (16, 56, 56)))
+    a = ref.angles(pos.cpu().numpy(), (16, 56, 56), (1e4,) * 3)
+    err = np.abs(got - np.stack([np.cos(a), np.sin(a)], -1))
+    assert np.all(err <= 1e-7 + np.abs(a)[..., None] * 2.0 ** -50), err.max()
+
+
 def test_rope_table_of_packed_positions_and_branches():
     grids = [T.TokenGrid(frames=7), T.TokenGrid(3, 4, 5, origin=(7.0, 0.0, 0.0),
                                                 frame_step=(4 / 24, 0, 0))]
