@@ -315,6 +315,50 @@ def test_linear_of_a_long_sequence(B, N, heads_in):
     assert bool(torch.isfinite(y).all())
 
 
+def on_gpu(shape, dtype, seed, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(DT[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("act", [None, "gelu", "gelu_tanh", "silu"])
+def test_linear_of_a_long_sequence_in_every_form(dtype, act):
+    # the 512 x 256 tiles of every type and activation; sampled rows and columns
+    N, K, C = 20000, 4096, 8192
+    x, w = on_gpu((1, N, K), dtype, 61), on_gpu((C, K), dtype, 62, K ** -0.5)
+    o = {"bias": rand((C,), dtype, 63, 0.3), "gate": rand((1, C), dtype, 64, 0.5, 0.5),
+         "residual": on_gpu((1, N, C), dtype, 65)}
+    y = T.linear(x, w, act=act, **o)
+    assert T.device_status() == 0
+    rows = torch.tensor([0, 127, 128, 255, 256, 511, 512, N // 2, N - 33, N - 32, N - 1], device="cuda")
+    cols = torch.cat([torch.arange(c, c + 24, device="cuda") for c in (0, 120, 250, 4000, C - 24)])
+    part = {"bias": o["bias"][cols], "gate": o["gate"][:, cols],
+            "residual": o["residual"][:, rows][:, :, cols]}
+    value, bound = linear_ref(x[:, rows], w[cols], part, act)
+    close(y[:, rows][:, :, cols], value, bound, dtype)
+    assert bool(torch.isfinite(y).all())
+
+
+@pytest.mark.parametrize("N,C", [(64, 7168), (566, 7168), (20000, 8192)])
+def test_sums_lose_nothing_systematically(N, C):
+    # 7,168 products through fp16 against 64 bits.  The last rounding is exactly that of the exact
+    # value but for its ties, so what goes beyond it comes from the sums: 448 steps of 16 products,
+    # each of which may cut off up to two units (2^-23) of a partial sum no larger, on average, than
+    # the result.  As a mean over the signs this is 1.1e-4 of the mean magnitude, an order below
+    # what the elementwise bound lets pass, and the last rounding averages out (below 1e-6 here).
+    K = 7168
+    x, w = on_gpu((N, K), "fp16", 71), on_gpu((C, K), "fp16", 72, K ** -0.5)
+    y = T.linear(x, w)
+    assert T.device_status() == 0
+    rows = torch.arange(0, N, max(1, N // 512), device="cuda")
+    exact = x[rows].double() @ w.double().t()
+    err, rounding = y[rows].double() - exact, exact.half().double() - exact
+    lost = K // 16 * 2 * 2.0 ** -23
+    assert abs(float((err * exact.sign()).mean() / exact.abs().mean())) <= lost + 2e-6
+    rms = lambda t: float(t.square().mean().sqrt())
+    assert rms(err) <= rms(rounding) + lost * rms(exact)
+
+
 def test_linear_keeps_bad_rows_apart():
     # infinities and NaN of one token stay in its row
     for N in (6, 300):
@@ -445,6 +489,23 @@ def test_qkv_project_of_a_long_sequence(halves):
         value, bound = (v[i], e[i]) if i == 2 else ref.norm_rope(
             v[i], np64(wq), float(np.float32(1e-6)), True, np64(table[rows]), halves, e[i])
         close(out[i][0][:, rows], value, bound, "bf16")
+        assert bool(torch.isfinite(out[i]).all())
+
+
+def test_qkv_project_of_a_long_sequence_fp16():
+    N, K, H, D = 20100, 4096, 21, 128
+    x, w = on_gpu((1, N, K), "fp16", 81), on_gpu((3 * H * D, K), "fp16", 82, K ** -0.5)
+    wq = rand((H, D), "fp16", 83, 0.2, 1.0)
+    table = table_for(N, (16, 24, 24), 84)
+    out = T.qkv_project(x, w, H, None, wq, wq, table=table, pairing="halves")
+    assert T.device_status() == 0
+    rows = torch.tensor([0, 31, 32, 255, 256, 511, 512, N // 2, N - 132, N - 1], device="cuda")
+    v, e = ref.product(np64(x[0, rows]), np64(w), None)
+    v, e = (a.reshape(len(rows), 3, H, D).transpose(1, 2, 0, 3) for a in (v, e))
+    for i in range(3):
+        value, bound = (v[i], e[i]) if i == 2 else ref.norm_rope(
+            v[i], np64(wq)[:, None, :], float(np.float32(1e-6)), True, np64(table[rows]), True, e[i])
+        close(out[i][0][:, rows], value, bound, "fp16")
         assert bool(torch.isfinite(out[i]).all())
 
 
