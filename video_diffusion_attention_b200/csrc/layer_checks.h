@@ -71,8 +71,8 @@ inline bool same_shape(const tara_view& a, const tara_view& b) {
   return a.B == b.B && a.H == b.H && a.N == b.N && a.D == b.D;
 }
 
-// The norm and rotation of heads [H][D]; `align`: bytes of the weights' and table's alignment.
-inline int check_norm_rope(const tara_norm_rope* p, int H, int D, int N, tara_dtype dt) {
+// The norm and rotation of heads of D columns and N tokens.
+inline int check_norm_rope(const tara_norm_rope* p, int D, int N, tara_dtype dt) {
   if (p->norm != 0 && p->norm != 1) return TARA_ERR_PARAM;
   if (!p->norm && !p->table) return TARA_ERR_PARAM;
   if (p->norm) {
@@ -93,7 +93,6 @@ inline int check_norm_rope(const tara_norm_rope* p, int H, int D, int N, tara_dt
       return TARA_ERR_PARAM;
     if (!ptr_aligned(p->table, 16) || p->table_batch_stride % 4 != 0) return TARA_ERR_ALIGN;
   }
-  (void)H;
   return TARA_OK;
 }
 

@@ -68,8 +68,9 @@ __device__ __forceinline__ void activate_pair(float& v0, float& v1) {
   if (kAct == 1) {
     // v/2 (1 + erf(v / sqrt 2)) = v Phi(v), with Phi from erfc(x) = t exp(-x^2 + P(t)),
     // t = 1 / (1 + x/2), x = |v| / sqrt 2: the form of Numerical Recipes' erfcc, P a polynomial
-    // of degree 9 in t fitted to ln(erfc(x) exp(x^2) / t) on 0 <= x <= 10 by Lawson's iteration
-    // (largest error 4.5e-8), in log2 units here.  The tail keeps its relative accuracy.
+    // of degree 9 in t fitted to ln(erfc(x) exp(x^2) / t) on 0 <= x <= 10 by Lawson's iteration,
+    // in log2 units here (largest error of the logarithm, coefficients as stored: 7.9e-8).  The
+    // tail keeps its relative accuracy: in fp32 within 9e-6 down to v = -12.8.
     float d0, d1, e0, e1;
     f32x2_unpack(f32x2_fma(f32x2_pack(fminf(fabsf(v0), 64.f), fminf(fabsf(v1), 64.f)),
                            both(0.35355339059f), both(1.f)), d0, d1);

@@ -2,7 +2,7 @@
 //
 // Bound by reading W once (2*C*K bytes; at one row an operation a byte, at 128 rows half the
 // tensor rate of the measured ridge).  So the roles are swapped: 128 rows of W are the M = 128
-// operand of tcgen05.mma, kT tokens (16 to 128) the N operand, and no lane of the tensor core
+// operand of tcgen05.mma, kT tokens (16 to 256) the N operand, and no lane of the tensor core
 // multiplies padding when there is one token.  K is split over the CTAs of a cluster, so that C/128
 // tiles still fill the device; each keeps a ring of 16 KB weight tiles in flight (up to three CTAs an
 // SM, so that one streams while another starts or ends).

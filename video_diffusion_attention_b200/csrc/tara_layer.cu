@@ -348,8 +348,9 @@ int run_linear(LinearArgs a, const HeadArgs* head, tara_dtype dt, cudaStream_t s
   if (head) p.head = *head;
   // Tile width by the estimated cycles of a cluster's rounds.  A 64-column K step of a 256 x bn
   // tile takes 2 * bn cycles of the tensor cores, and its (256 + bn) * 64 bytes an SM arrive at
-  // about 64 bytes a cycle, which is the larger up to 256 columns.  What a round costs beyond its
-  // products (filling the ring, the last tile's epilogue) counts as 8 K steps.  Widths between
+  // about 64 bytes a cycle, which is the larger up to 256 columns.  What a call costs beyond its
+  // products (filling the ring, the last tile's epilogue; the epilogues of earlier rounds run
+  // under the next products) counts as 8 K steps.  Widths between
   // 128 and 256 are for rows of one head and one part, where a tile may end anywhere (512 x 7,168
   // -> 7,168 on 74 SM pairs: 70 tiles of 208 columns, 42 us, instead of 56 of 256, 44 us).
   const int pairs = std::max(1, dev.sms / 2);
@@ -368,9 +369,15 @@ int run_linear(LinearArgs a, const HeadArgs* head, tara_dtype dt, cudaStream_t s
   }
   // 512 x 256 reads a quarter less through L2 than 256 x 256, but its accumulators fill tensor
   // memory, so part of every epilogue is exposed (about 5,000 cycles).  Long calls run at the
-  // power cap, where the saved traffic counts for more: 107,126 x 7,168 -> 7,168 back to back
-  // takes 8.7 ms against 9.3; with 1,024 input columns the exposed epilogue loses (1.05 against
-  // 0.69 ms).
+  // power cap, where the saved traffic counts for more.  Back to back for half a second each,
+  // 512-row against 256-row tiles, by K steps and rounds of 256 x 256 tiles:
+  //   112 steps: 24 rounds 1.33 and 1.35 ms, 48 rounds 2.63 and 2.72, 78 rounds 4.34 and 4.5,
+  //     158 rounds 9.2 and 10.2, 475 rounds 28.0 and 33.4;
+  //   88 steps, 158 rounds: 6.9 and 7.5 ms;
+  //   64 steps: 34 rounds 1.10 and 1.06 ms, 78 rounds 2.49 and 2.47, 158 rounds 5.0 and 5.1,
+  //     475 rounds 14.9 and 17.8;
+  //   32 steps, 78 rounds: 1.31 and 1.21 ms.
+  // The rule starts where the two meet.
   const bool tall = k_steps >= 64 && tiles128 / 2 >= 32LL * pairs;
   if (tall) p.bn = 256;
   const bool narrow = p.bn == 128;
@@ -441,7 +448,7 @@ int tara_qk_norm_rope(const tara_view* q, const tara_view* k, const tara_norm_ro
   }
   if (q->D % 8 != 0 || q->D > 256) return TARA_ERR_HEAD_DIM;
   if (2LL * q->H > 65535) return TARA_ERR_TOO_LARGE;
-  if ((rc = check_norm_rope(p, q->H, q->D, q->N, q->dtype)) != TARA_OK) return rc;
+  if ((rc = check_norm_rope(p, q->D, q->N, q->dtype)) != TARA_OK) return rc;
   // an output is its own input, or starts elsewhere than every other view
   if (q_out->ptr == q->ptr && !same_layout(*q_out, *q)) return TARA_ERR_PARAM;
   if (k) {
@@ -512,7 +519,7 @@ int tara_qkv_project(const tara_view* x, const void* w, const void* bias,
   if (2LL * q->H > 65535 || 3 * columns(*q) > 0x7fffffffLL) return TARA_ERR_TOO_LARGE;
   const uintptr_t align = x->dtype == TARA_FP32 ? 4 : 16;
   if (!ptr_aligned(w, align) || !ptr_aligned(bias, align)) return TARA_ERR_ALIGN;
-  if (p && (rc = check_norm_rope(p, q->H, q->D, q->N, q->dtype)) != TARA_OK) return rc;
+  if (p && (rc = check_norm_rope(p, q->D, q->N, q->dtype)) != TARA_OK) return rc;
   LinearArgs a{};
   a.x = row_view(*x);
   for (int i = 0; i < 3; ++i) a.y[i] = row_view(*outs[i]);
