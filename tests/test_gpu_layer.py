@@ -649,6 +649,70 @@ def test_streams_side_by_side(N):
         assert torch.equal(y, want) and torch.equal(z, want_q)
 
 
+FIRST_CALL = """
+import sys, torch
+import video_diffusion_attention_b200 as T
+rows = {"few": 3, "many": 300}.get(sys.argv[2], 40)
+x = torch.randn(1, rows, 256, device="cuda", dtype=getattr(torch, sys.argv[1]))
+w = torch.randn(768, 256, device="cuda").to(x.dtype)
+call = {"table": lambda: T.rope_table(torch.ones(40, 2, device="cuda"), (32, 32)),
+        "norm": lambda: T.qk_norm_rope(x.view(1, 40, 4, 64).transpose(1, 2)),
+        "few": lambda: T.linear(x, w, act="silu"),
+        "many": lambda: T.qkv_project(x, w, 4)[0]}[sys.argv[2]]
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    y = call()
+graph.replay()
+assert torch.equal(y, call()) and T.device_status() == 0
+"""
+
+
+@pytest.mark.parametrize("dtype,what", [("bfloat16", "few"), ("float16", "many"), ("float32", "few"),
+                                        ("bfloat16", "norm"), ("float32", "table")])
+def test_a_first_call_may_be_captured(dtype, what):
+    # a process whose first call of the library is recorded into a graph
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", FIRST_CALL, dtype, what], cwd=root, check=True, timeout=300)
+
+
+def test_calls_from_several_threads():
+    # the host side keeps what it looks up once a device; every thread has a stream of its own
+    import threading
+    x, w, o = linear_inputs(1, 300, 512, 768, "fp16", 4, "bgr")
+    few = x[:, :, :5]
+    few_o = dict(o, residual=o["residual"][:, :5])
+    f32 = x.float()
+    calls = [lambda: T.linear(x, w, act="silu", **o), lambda: T.linear(few, w, act="gelu", **few_o),
+             lambda: T.qkv_project(x, w, 4)[1], lambda: T.qk_norm_rope(x, f32.half())[1],
+             lambda: T.qk_norm_rope(f32)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    got, errors = {}, []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got[i] = [[c() for c in calls] for _ in range(20)]
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:      # raised again below
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors and len(got) == 4
+    for runs in got.values():
+        for run in runs:
+            assert all(torch.equal(a, b) for a, b in zip(run, want))
+    assert T.device_status() == 0
+
+
 def test_offsets_past_32_bits():
     # more than 2^31 elements: an output of the linear layer, then the norm in place
     N, K, C = 70001, 64, 32768
