@@ -5,7 +5,8 @@ Q/K/V projection.
 Tensors are CUDA tensors of one dtype (bf16, fp16 or fp32) on one device with the last dimension
 contiguous; other strides are passed on, so a part of a fused projection, a transposed view or
 rows of a packed tensor needs no copy.  Outputs the caller does not give are allocated on the
-stream the call runs on.
+stream the call runs on.  Forward only, like the attention: nothing is recorded for a gradient, and
+results do not require one.
 """
 from __future__ import annotations
 
