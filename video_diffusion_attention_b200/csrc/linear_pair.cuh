@@ -741,7 +741,7 @@ linear_pair_kernel(const __grid_constant__ PairLinMaps maps,
   if (threadIdx.x == 0) {
     mbar_arrive_cluster(mapa_shared(smem_u32(exit_bar), rank ^ 1u));
     volatile int no_abort = 0;
-    mbar_wait(exit_bar, 0, &no_abort, kLinWaitNs);
+    mbar_wait(exit_bar, 0, &no_abort, kLinExitNs);
     if (*abort_flag) atomicExch(a.status, 1);
   }
   __syncthreads();

@@ -49,6 +49,11 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 constexpr uint64_t kLinWaitNs = 2000000000ull;    // 2 s per wait; a normal wait is microseconds
 constexpr uint32_t kLinIdleNs = 1000000u;           // 1 ms between looks at the clock
 constexpr uint64_t kLinDrainNs = 200000000ull;    // 0.2 s to let in-flight MMAs land
+// A CTA that gives up leaves its pair's ring at once; the other starves from then on, gives up a
+// whole wait later, drains, and only then arrives on the first one's exit barrier, in shared memory
+// that has to be there still.  So the wait before the exit outlasts all of that.
+constexpr uint64_t kLinExitNs = 6000000000ull;
+static_assert(kLinExitNs >= 2 * (kLinWaitNs + kLinDrainNs), "the peer's last wait ends first");
 
 // One try of up to `hint_ns`: the thread is suspended by the hardware, not polling, until the
 // phase completes or the hint runs out.
